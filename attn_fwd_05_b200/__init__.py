@@ -11,6 +11,8 @@ from .binding import (  # noqa: F401
     attn_bwd,
     attn_bwd_workspace_size,
     attn_decode_paged,
+    attn_decode_paged_kv4,
+    attn_decode_paged_kv4_workspace_size,
     attn_decode_paged_noalloc,
     attn_decode_paged_workspace_size,
     attn_fwd,
@@ -18,6 +20,12 @@ from .binding import (  # noqa: F401
     attn_fwd_fp8,
     attn_fwd_masked,
     attn_get_device_status,
+    attn_kv4_append,
+    attn_kv4_gather,
+    attn_kv4_page_bytes,
+    attn_pages_compact,
+    attn_pages_fork,
+    attn_pages_workspace_size,
     attn_quantize_fp8,
     attn_debug_bwd_stall,
     attn_debug_decode_stall,

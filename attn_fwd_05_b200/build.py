@@ -2,7 +2,7 @@
 
     python -m attn_fwd_05_b200.build [--verbose]
 
-The library is one translation unit (csrc/attn_api.cu) linked against the static CUDA
+The library is one translation unit (csrc/attn_b200.cu) linked against the static CUDA
 runtime; the TMA descriptor encoder is reached through the runtime's driver entry
 point, so no libcuda link is needed at build time.
 """
@@ -16,7 +16,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "attn_api.cu")
+SRC = os.path.join(HERE, "csrc", "attn_b200.cu")
 DEPS = [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join(HERE, "csrc"))] + [
     os.path.join(ROOT, "include", "attn_b200.h")]
 OUT = os.path.join(HERE, "libattn_b200.so")

@@ -2,7 +2,7 @@
 //
 // Host side only: argument checks, TMA tensor-map encoding, launch configuration.
 // Every step of the computation runs in the kernels of prefill_sm100.cuh and
-// decode_sm100.cuh.  The whole library is this one translation unit.
+// decode_sm100.cuh.  The library's translation unit is attn_b200.cu, which includes this file.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -1,0 +1,386 @@
+// cache_api.cuh — host side of the 4-bit cache and page entry points of include/attn_b200.h:
+// argument checks, workspace layouts and launches.  Included by attn_b200.cu after attn_api.cu,
+// whose helpers (aligned, sm_count, ensure_smem, launch_status, align256) it uses.
+#pragma once
+
+#include "decode_kv4_sm100.cuh"
+#include "kv4_sm100.cuh"
+#include "pages_sm100.cuh"
+
+namespace {
+
+bool kv4_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
+bool cache_page_size(int p) { return p == 16 || p == 32 || p == 64; }
+
+// Sizes shared by the entry points that read a table into a 4-bit pool.  Record numbers fit an int.
+attn_status kv4_check(const void* pool, const int32_t* table, const int32_t* seq_lens, int page_size, int S, int Hkv,
+                      int d, int num_pages, int max_pages) {
+  if (S < 0 || Hkv <= 0 || num_pages < 0 || max_pages <= 0) return ATTN_ERR_INVALID_ARG;
+  if (!kv4_head_dim(d) || !cache_page_size(page_size)) return ATTN_ERR_UNSUPPORTED;
+  if (S == 0) return ATTN_OK;
+  if (table == nullptr || seq_lens == nullptr || (num_pages > 0 && pool == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(table, 4) || !aligned(seq_lens, 4) || (num_pages > 0 && !aligned(pool, 16))) return ATTN_ERR_ALIGNMENT;
+  if ((long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if (num_pages > 0x7fffffffLL / Hkv / (page_size / attn::kKv4Tok)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+template <int NG>
+attn_status launch_append(const attn::Kv4AppendArgs& a, unsigned grid, cudaStream_t st) {
+  attn::attn_kv4_append_kernel<NG><<<grid, 256, 0, st>>>(a);
+  return launch_status();
+}
+
+template <int NG>
+attn_status launch_gather(const attn::Kv4GatherArgs& a, unsigned grid, cudaStream_t st) {
+  attn::attn_kv4_gather_kernel<NG><<<grid, 256, 0, st>>>(a);
+  return launch_status();
+}
+
+struct DecKv4Layout {
+  size_t off_lse, off_o, total;
+  long long warps;
+};
+
+// Query heads of a segment: 8 columns of an MMA, or 16 where a group has more than 8 heads and
+// the accumulators leave room.
+int kv4_head_tiles(int group, int d) { return group > 8 && d <= 128 ? 2 : 1; }
+
+DecKv4Layout kv4_layout(int S, int group, int d) {
+  DecKv4Layout L;
+  const int nt = kv4_head_tiles(group, d);
+  L.warps = (long long)sm_count() * (d * nt <= 128 ? 4 : 2) * 4;
+  L.off_lse = align256((size_t)(S + 2) * 8);
+  L.off_o = L.off_lse + align256((size_t)L.warps * 2 * 8 * nt * 4);
+  L.total = L.off_o + (size_t)L.warps * 2 * 8 * nt * d * 4;
+  return L;
+}
+
+template <int D, int NT>
+attn_status launch_decode_kv4(const attn::DecKv4Args& a, cudaStream_t st, int slot) {
+  using C = attn::DecKv4Cfg<D, NT>;
+  auto k = attn::attn_decode_kv4_split_kernel<D, NT>;
+  if (!ensure_smem(k, C::SMEM, slot)) return ATTN_ERR_CUDA;
+  // no more CTAs than the longest possible rows can feed
+  const double ctas = std::ceil((double)a.S * a.max_pages * (1 << a.lg_blocks) * a.Hkv * a.n_hg /
+                                (C::WARPS * attn::kDecKv4MinTiles));
+  const int grid = (int)std::max(1.0, std::min(ctas, (double)sm_count() * C::CTAS_PER_SM));
+  k<<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  const long long rows = (long long)a.S * a.Hq;
+  attn::attn_decode_kv4_merge_kernel<D, NT><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
+  return launch_status();
+}
+
+struct PagesLayout {
+  size_t off[8], zero_bytes, total;
+};
+
+// Workspace of both page operators, in the order of the marks (cleared first) and the lists.
+PagesLayout pages_layout(int num_pages, int rows) {
+  PagesLayout L;
+  const size_t words = align256(((size_t)num_pages + 31) / 32 * 4), ids = align256((size_t)num_pages * 4),
+               per_row = align256((size_t)rows * 4);
+  const size_t sizes[8] = {words, words, ids, ids, per_row, per_row, per_row, per_row};
+  size_t at = 256;  // counts
+  for (int i = 0; i < 8; ++i) {
+    L.off[i] = at;
+    at += sizes[i];
+  }
+  L.zero_bytes = 2 * words;
+  L.total = at;
+  return L;
+}
+
+attn_status pools_check(void* const* pools, int n_pools, size_t page_bytes, int num_pages, attn::PagePools* out) {
+  if (n_pools < 0 || (n_pools > 0 && pools == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (n_pools > attn::kMaxPools) return ATTN_ERR_TOO_LARGE;
+  if (page_bytes % 16 != 0 || page_bytes > (size_t(1) << 40)) return ATTN_ERR_INVALID_ARG;
+  std::memset(out, 0, sizeof(*out));
+  for (int i = 0; i < n_pools; ++i) {
+    if (num_pages > 0 && page_bytes > 0 && pools[i] == nullptr) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(pools[i], 16)) return ATTN_ERR_ALIGNMENT;
+    out->base[i] = static_cast<uint8_t*>(pools[i]);
+  }
+  out->n = page_bytes > 0 ? n_pools : 0;
+  out->page_bytes = (long long)page_bytes;
+  return ATTN_OK;
+}
+
+// CTAs that share one page copy: one for every 16 KB, up to 32.
+int copy_parts(size_t page_bytes) {
+  return (int)std::max<size_t>(1, std::min<size_t>(32, page_bytes / 16384));
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_kv4_page_bytes(int Hkv, int page_size, int d) {
+  if (Hkv <= 0 || !kv4_head_dim(d) || !cache_page_size(page_size)) return 0;
+  return (size_t)Hkv * (page_size / attn::kKv4Tok) * attn::kv4_record_bytes(d);
+}
+
+attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, void* kv_pool,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_new, int page_size,
+                            void* k_out, void* v_out, int num_seqs, int num_new, int Hkv, int d, int num_pages,
+                            int max_pages_per_seq, void* stream) {
+  const attn_status chk =
+      kv4_check(kv_pool, block_table, seq_lens, page_size, num_seqs, Hkv, d, num_pages, max_pages_per_seq);
+  if (chk != ATTN_OK) return chk;
+  if (num_new < 0 || (num_seqs == 0 && num_new > 0)) return ATTN_ERR_INVALID_ARG;
+  if (num_new == 0) return ATTN_OK;
+  if (k == nullptr || v == nullptr || cu_new == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (k_stride < (int64_t)Hkv * d || v_stride < (int64_t)Hkv * d) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_new, 4) || (k_out && !aligned(k_out, 16)) ||
+      (v_out && !aligned(v_out, 16)) || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return ATTN_ERR_ALIGNMENT;
+  attn::Kv4AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.pool = static_cast<uint8_t*>(kv_pool);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.cu_new = cu_new;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.S = num_seqs;
+  a.T = num_new;
+  a.Hkv = Hkv;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  const long long units = ((long long)(num_new >> 2) + 2ll * num_seqs) * Hkv;
+  const long long grid = (units + 7) / 8;
+  if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (d) {
+    case 64: return launch_append<1>(a, (unsigned)grid, st);
+    case 128: return launch_append<2>(a, (unsigned)grid, st);
+    default: return launch_append<4>(a, (unsigned)grid, st);
+  }
+}
+
+attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, const int32_t* seq_lens, int page_size,
+                            void* k, void* v, int num_seqs, int Hkv, int N, int d, int num_pages,
+                            int max_pages_per_seq, void* stream) {
+  const attn_status chk =
+      kv4_check(kv_pool, block_table, seq_lens, page_size, num_seqs, Hkv, d, num_pages, max_pages_per_seq);
+  if (chk != ATTN_OK) return chk;
+  if (N < 0) return ATTN_ERR_INVALID_ARG;
+  if (num_seqs == 0 || N == 0) return ATTN_OK;
+  if (k == nullptr || v == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_ALIGNMENT;
+  attn::Kv4GatherArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.pool = static_cast<const uint8_t*>(kv_pool);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.k = static_cast<__nv_bfloat16*>(k);
+  a.v = static_cast<__nv_bfloat16*>(v);
+  a.S = num_seqs;
+  a.Hkv = Hkv;
+  a.N = N;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  // N may be larger than any row: records past a row's capacity have no work
+  const long long nrec = ((long long)N + 15) / 16;
+  const long long units = nrec * num_seqs;
+  if (units > 0x7fffffffLL * 8 / Hkv) return ATTN_ERR_INVALID_ARG;
+  const unsigned grid = (unsigned)((units * Hkv + 7) / 8);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (d) {
+    case 64: return launch_gather<1>(a, grid, st);
+    case 128: return launch_gather<2>(a, grid, st);
+    default: return launch_gather<4>(a, grid, st);
+  }
+}
+
+size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d) {
+  if (num_seqs < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || !kv4_head_dim(d)) return 0;
+  return kv4_layout(num_seqs, Hq / Hkv, d).total;
+}
+
+attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int32_t* block_table,
+                                  const int32_t* seq_lens, int page_size, void* o, float* lse, int num_seqs, int Hq,
+                                  int Hkv, int d, int num_pages, int max_pages_per_seq, float scale, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  const attn_status chk =
+      kv4_check(kv_pool, block_table, seq_lens, page_size, num_seqs, Hkv, d, num_pages, max_pages_per_seq);
+  if (chk != ATTN_OK) return chk;
+  if (num_seqs == 0) return ATTN_OK;
+  if (q == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || (lse != nullptr && !aligned(lse, 4))) return ATTN_ERR_ALIGNMENT;
+  if ((long long)num_seqs * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  const int group = Hq / Hkv;
+  const DecKv4Layout L = kv4_layout(num_seqs, group, d);
+  if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  attn::DecKv4Args a;
+  std::memset(&a, 0, sizeof(a));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.pool = static_cast<const uint8_t*>(kv_pool);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.tile_prefix = reinterpret_cast<long long*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + L.off_lse);
+  a.part_o = reinterpret_cast<float*>(ws + L.off_o);
+  a.S = num_seqs;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.group = group;
+  const int nt = kv4_head_tiles(group, d);
+  a.n_hg = (group + 8 * nt - 1) / (8 * nt);
+  a.page_size = page_size;
+  a.lg_blocks = page_size == 16 ? 0 : (page_size == 32 ? 1 : 2);
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (d) {
+    case 64: return nt == 1 ? launch_decode_kv4<64, 1>(a, st, 20) : launch_decode_kv4<64, 2>(a, st, 21);
+    case 128: return nt == 1 ? launch_decode_kv4<128, 1>(a, st, 22) : launch_decode_kv4<128, 2>(a, st, 23);
+    default: return launch_decode_kv4<256, 1>(a, st, 24);
+  }
+}
+
+size_t attn_pages_workspace_size(int num_pages, int rows) {
+  if (num_pages < 0 || rows < 0) return 0;
+  return pages_layout(num_pages, rows).total;
+}
+
+attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                            const int32_t* add_tokens, int32_t* new_table, int32_t* new_lens, int page_size,
+                            void* const* pools, int n_pools, size_t page_bytes, int num_seqs, int max_pages_per_seq,
+                            int new_rows, int new_max_pages, int num_pages, int32_t* n_free, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0 || new_rows < 0 || max_pages_per_seq <= 0 || new_max_pages < max_pages_per_seq || num_pages < 0 ||
+      page_size <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if ((long long)new_max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  attn::PagePools pp;
+  const attn_status chk = pools_check(pools, n_pools, page_bytes, num_pages, &pp);
+  if (chk != ATTN_OK) return chk;
+  const size_t in_bytes = (size_t)num_seqs * max_pages_per_seq * 4, out_bytes = (size_t)new_rows * new_max_pages * 4;
+  if ((num_seqs > 0 && (block_table == nullptr || seq_lens == nullptr)) ||
+      (new_rows > 0 && (parents == nullptr || new_table == nullptr || new_lens == nullptr)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(add_tokens, 4) ||
+      !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(n_free, 4))
+    return ATTN_ERR_ALIGNMENT;
+  // rows are read while others are written
+  if (overlap(block_table, in_bytes, new_table, out_bytes) ||
+      overlap(seq_lens, (size_t)num_seqs * 4, new_lens, (size_t)new_rows * 4) ||
+      overlap(parents, (size_t)new_rows * 4, new_lens, (size_t)new_rows * 4) ||
+      overlap(add_tokens, (size_t)new_rows * 4, new_lens, (size_t)new_rows * 4))
+    return ATTN_ERR_INVALID_ARG;
+  const PagesLayout L = pages_layout(num_pages, new_rows);
+  if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  attn::ForkArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.add = add_tokens;
+  a.new_table = new_table;
+  a.new_lens = new_lens;
+  a.n_free = n_free;
+  a.n_list = reinterpret_cast<int*>(ws);
+  a.full_bits = reinterpret_cast<uint32_t*>(ws + L.off[0]);
+  a.part_bits = reinterpret_cast<uint32_t*>(ws + L.off[1]);
+  a.first_part = reinterpret_cast<int*>(ws + L.off[2]);
+  a.free_list = reinterpret_cast<int*>(ws + L.off[3]);
+  a.row_part = reinterpret_cast<int*>(ws + L.off[4]);
+  a.row_fresh = reinterpret_cast<int*>(ws + L.off[5]);
+  a.row_rank = reinterpret_cast<int*>(ws + L.off[6]);
+  a.row_keep = reinterpret_cast<int*>(ws + L.off[7]);
+  a.S = num_seqs;
+  a.cols = max_pages_per_seq;
+  a.rows = new_rows;
+  a.new_cols = new_max_pages;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  if (cudaMemsetAsync(ws + L.off[0], 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (num_pages > 0 && cudaMemsetAsync(a.first_part, 0x7f, (size_t)num_pages * 4, st) != cudaSuccess)
+    return ATTN_ERR_CUDA;  // 0x7f7f7f7f: above every row number in use here
+  if (new_rows > 0) {
+    attn::attn_pages_fork_mark_kernel<<<(unsigned)new_rows, attn::kPagesThreads, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  }
+  attn::attn_pages_fork_scan_kernel<<<1, attn::kScanThreads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (new_rows == 0) return ATTN_OK;
+  const int parts = copy_parts(page_bytes);
+  const dim3 grid((unsigned)new_rows, (unsigned)std::max(1, std::min(pp.n * parts, 1024)));
+  attn::attn_pages_fork_move_kernel<<<grid, attn::kPagesThreads, 0, st>>>(a, pp, parts);
+  return launch_status();
+}
+
+attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_lens, int32_t* new_table,
+                               int32_t* page_map, int page_size, void* const* pools, int n_pools, size_t page_bytes,
+                               int num_seqs, int max_pages_per_seq, int num_pages, int32_t* n_live, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0 || max_pages_per_seq <= 0 || num_pages < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  attn::PagePools pp;
+  const attn_status chk = pools_check(pools, n_pools, page_bytes, num_pages, &pp);
+  if (chk != ATTN_OK) return chk;
+  if ((num_seqs > 0 && (block_table == nullptr || seq_lens == nullptr || new_table == nullptr)) ||
+      (num_pages > 0 && page_map == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(new_table, 4) || !aligned(page_map, 4) ||
+      !aligned(n_live, 4))
+    return ATTN_ERR_ALIGNMENT;
+  const size_t bytes = (size_t)num_seqs * max_pages_per_seq * 4;
+  if (block_table != new_table && overlap(block_table, bytes, new_table, bytes)) return ATTN_ERR_INVALID_ARG;
+  const PagesLayout L = pages_layout(num_pages, num_seqs);
+  if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  attn::CompactArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.new_table = new_table;
+  a.page_map = page_map;
+  a.n_live = n_live;
+  a.counts = reinterpret_cast<int*>(ws);
+  a.bits = reinterpret_cast<uint32_t*>(ws + L.off[0]);
+  a.prefix = reinterpret_cast<int*>(ws + L.off[1]);
+  a.src = reinterpret_cast<int*>(ws + L.off[2]);
+  a.dst = reinterpret_cast<int*>(ws + L.off[3]);
+  a.S = num_seqs;
+  a.cols = max_pages_per_seq;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  if (cudaMemsetAsync(a.bits, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (num_seqs > 0) {
+    attn::attn_pages_compact_mark_kernel<<<(unsigned)num_seqs, attn::kPagesThreads, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  }
+  attn::attn_pages_compact_scan_kernel<<<1, attn::kScanThreads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  attn::attn_pages_compact_move_kernel<<<(unsigned)(sm_count() * 8), attn::kPagesThreads, 0, st>>>(
+      a, pp, copy_parts(page_bytes));
+  return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,628 @@
+// decode_kv4_sm100.cuh — one decode step over a paged K/V cache held in 4 bits, for sm_100a.
+//
+// What is computed is attn_decode_paged's softmax(scale q K^T) V with K and V standing for the
+// cache's values x = s c + m (kv4_sm100.cuh).  The step has to read d * 9/8 bytes per cached
+// token and KV head, 3.6 times fewer than the bf16 cache, so the arithmetic on those bytes is
+// what has to keep up with HBM, and the kernel is built around its instruction count:
+//
+//   * The codes are the A operand (16 rows) of m16n8k16 MMAs and up to 8 query heads of the KV
+//     group the 8 columns: S^T = K q^T has 16 tokens as rows, O^T = V^T P^T 16 channels, so no
+//     row of a product is padding.  The records hold the codes in that operand's order.
+//   * A 4-bit code becomes an fp16 operand without a conversion: masked into the mantissa of
+//     1024 it is 1024 + c (or 1024 + 16 c, one nibble further up), and one fp16 FMA makes c - 8
+//     of it, exactly.  K's scale and minimum are applied to the fp32 products,
+//         q . K_j = sum_y s_jy (q_y . (c - 8)_jy) + (m_jy + 8 s_jy) sum(q_y),
+//     V's scale goes into the probabilities and its minimum into one sum per head and group,
+//         O_y = sum_j (p_j s_jy) (c - 8)_jy + sum_j p_j (m_jy + 8 s_jy).
+//     Centring the codes keeps the rounding of p s (fp16, 11 bits) multiplied by the small signed
+//     code instead of by an offset that the second sum would have to cancel.
+//   * fp16 range: q is scaled by a power of two per head (its bf16 significand fits fp16's);
+//     p s is scaled by a power of two per channel group that follows the largest V scale seen.
+//   * P^T reaches the B operand's layout with two 8x8 transposes (movmatrix) per group.
+//   * The running maximum is raised only when a score passes it by more than 2^8: one vote per
+//     16 tokens in place of six shuffles and a rescale.  P stays below 2^8 in between.
+//
+// Work split: the 16-token tiles of all (sequence, KV head, head group) segments form one
+// stream; every warp takes an equal contiguous range of it, whatever the lengths, and runs alone: it
+// fetches its records with 16-byte asynchronous copies into its own ring in shared memory and
+// never waits for another warp.  A segment that lies inside one warp's range is finished there; the
+// others leave partials (at most two per warp) that the merge kernel joins by log-sum-exp.
+#pragma once
+
+#include "kv4_sm100.cuh"
+
+namespace attn {
+
+struct DecKv4Args {
+  const __nv_bfloat16* q;      // [S, Hq, d]
+  const uint8_t* pool;         // [num_pages, Hkv, page_size / 16, record]
+  const int32_t* block_table;  // [S, max_pages]
+  const int32_t* seq_lens;     // [S]
+  __nv_bfloat16* o;            // [S, Hq, d]
+  float* lse;                  // [S, Hq] or null
+  long long* tile_prefix;      // workspace: [S + 1] tiles of the sequences before s, then the range length
+  float* part_o;               // workspace: [warps][2][8 NT][d]
+  float* part_lse;             // workspace: [warps][2][8 NT], log2 units
+  int S, Hq, Hkv, group, n_hg, page_size, lg_blocks, num_pages, max_pages;
+  float scale_log2;
+};
+
+template <int D, int NT>
+struct DecKv4Cfg {
+  static constexpr int NG = D / kKv4Group;
+  static constexpr int ROWS = 8 * NT;  // query heads of a segment
+  static constexpr int REC = kv4_record_bytes(D);
+  static constexpr int WARPS = 4;
+  static constexpr int CTAS_PER_SM = (D * NT <= 128) ? 4 : 2;
+  static constexpr int STAGES = (D == 64) ? 8 : 6;
+  static constexpr int SMEM = WARPS * STAGES * REC;
+  static constexpr int THREADS = WARPS * 32;
+};
+
+constexpr int kDecKv4MinTiles = 4;  // shortest range of a warp: 64 tokens
+
+// ------------------------------------------------------------------ fp16 and copy helpers
+
+// c += a b on a 16x8x16 tile, fp16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of 16-bit elements held by the warp (two neighbours of a row a lane).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+template <int N>  // N words, N = 1, 2 or 4
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The pairs (nibble i of the low half, nibble i of the high half) of a word as fp16 c - 8,
+// i = 0..3.  1024 + c - 1032 and (1024 + 16 c) / 16 - 72 are exact.
+__device__ __forceinline__ void kv4_centred(uint32_t w, uint32_t (&p)[4]) {
+  const uint32_t w8 = w >> 8;
+  uint32_t x0, x1, x2, x3;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(x0) : "r"(w));
+  asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(x1) : "r"(w));
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(x2) : "r"(w8));
+  asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(x3) : "r"(w8));
+  constexpr uint32_t kOne = 0x3c003c00u, kM1032 = 0xe408e408u;       // 1, -1032
+  constexpr uint32_t kSixteenth = 0x2c002c00u, kM72 = 0xd480d480u;  // 1/16, -72
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[0]) : "r"(x0), "r"(kOne), "r"(kM1032));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[1]) : "r"(x1), "r"(kSixteenth), "r"(kM72));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[2]) : "r"(x2), "r"(kOne), "r"(kM1032));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[3]) : "r"(x3), "r"(kSixteenth), "r"(kM72));
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Exponent of x >= 0, clamped to [-100, top]; of 0 the lower end, of infinity and NaN (which any
+// scaling keeps) the upper end.
+__device__ __forceinline__ int exponent_of(float x, int top) {
+  return min(top, max(-100, (int)((__float_as_uint(x) >> 23) & 0xffu) - 127));
+}
+
+__device__ __forceinline__ float max_over_rows(float x) {  // over the 8 rows of an MMA fragment column
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// ------------------------------------------------------------------ the work stream
+
+__device__ __forceinline__ int kv4_seq_len(const DecKv4Args& a, int s) {  // 0 for a length out of range
+  const int len = __ldg(&a.seq_lens[s]);
+  return len < 0 || len > a.max_pages * a.page_size ? 0 : len;
+}
+
+// A position in the stream: tile t of segment c (KV head and head group) of sequence s.
+struct Kv4Cursor {
+  int s, c, t, nt;
+  __device__ __forceinline__ void forward(const DecKv4Args& a, int n) {
+    t += n;
+    while (t >= nt && s < a.S) {
+      t -= nt;
+      if (++c == a.Hkv * a.n_hg) {
+        c = 0;
+        nt = 0;
+        while (++s < a.S && nt == 0) nt = (kv4_seq_len(a, s) + kKv4Tok - 1) / kKv4Tok;
+        if (nt > 0) --s;  // the loop's last increment passed the sequence found
+      }
+    }
+  }
+};
+
+// Finds the first tiles of this CTA's warps: first[w] = {s, c, t, tiles of the range} (0 tiles: no
+// work).  Every thread of the block calls it.  CTA 0 also leaves the tile prefix for the merge.
+template <int WARPS>
+__device__ __forceinline__ void kv4_plan(const DecKv4Args& a, int4* first, long long* warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int C = a.Hkv * a.n_hg;
+  const int per_thread = (a.S + WARPS * 32 - 1) / (WARPS * 32);
+  const int s0 = min(a.S, tid * per_thread), s1 = min(a.S, s0 + per_thread);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    mine += (kv4_seq_len(a, s) + kKv4Tok - 1) / kKv4Tok;
+    if (blockIdx.x == 0 && (__ldg(&a.seq_lens[s]) < 0 || __ldg(&a.seq_lens[s]) > a.max_pages * a.page_size))
+      latch_status(ATTN_ERR_INVALID_ARG);
+  }
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[wid] = x;
+  if (tid < WARPS) first[tid] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  long long before = x - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < wid) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  const long long T = total * C, warps = (long long)gridDim.x * WARPS;
+  const long long per = max((T + warps - 1) / warps, (long long)kDecKv4MinTiles);
+  for (int s = s0; s < s1; ++s) {
+    const int nt = (kv4_seq_len(a, s) + kKv4Tok - 1) / kKv4Tok;
+    if (blockIdx.x == 0) a.tile_prefix[s] = before;
+    const long long f0 = before * C, f1 = f0 + (long long)nt * C;
+    for (int w = 0; w < WARPS; ++w) {
+      const long long f = ((long long)blockIdx.x * WARPS + w) * per;
+      if (f >= f0 && f < f1)
+        first[w] = make_int4(s, (int)((f - f0) / nt), (int)((f - f0) % nt), (int)min(per, T - f));
+    }
+    before += nt;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.tile_prefix[a.S] = total;
+    a.tile_prefix[a.S + 1] = per;
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ split kernel
+
+template <int D, int NT>
+__global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::CTAS_PER_SM)
+    attn_decode_kv4_split_kernel(const __grid_constant__ DecKv4Args a) {
+  using C = DecKv4Cfg<D, NT>;
+  constexpr int NG = C::NG;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int4 first[C::WARPS];
+  __shared__ long long warp_sums[C::WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;  // row and column pair of the MMA fragments
+  kv4_plan<C::WARPS>(a, first, warp_sums);
+  const int4 f = first[warp];
+  const int n = f.w;
+  if (n == 0) return;
+  const int wslot = 2 * (blockIdx.x * C::WARPS + warp);
+  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::REC);
+
+  // ---- fetch side: lane l keeps the record number of tile l of the current batch of 32 tiles
+  // (-1: its page is out of range), and of the next batch, whose table loads are then in flight
+  // long before they are needed
+  Kv4Cursor fc{f.x, f.y, f.z, 0};
+  fc.nt = (kv4_seq_len(a, fc.s) + kKv4Tok - 1) / kKv4Tok;
+  fc.forward(a, lane);
+  auto record_of = [&](int tile) -> int {
+    if (tile >= n || fc.s >= a.S) return -1;
+    const int page = __ldg(&a.block_table[(size_t)fc.s * a.max_pages + (fc.t >> a.lg_blocks)]);
+    if (page < 0 || page >= a.num_pages) {
+      latch_status(ATTN_ERR_BAD_PAGE);
+      return -1;
+    }
+    const int kvh = fc.c / a.n_hg;
+    return ((page * a.Hkv + kvh) << a.lg_blocks) + (fc.t & ((1 << a.lg_blocks) - 1));
+  };
+  int rec_cur = record_of(lane);
+  fc.forward(a, 32);
+  int rec_next = n > 32 ? record_of(lane + 32) : -1;
+  uint32_t good = 0;  // bit i % 32: tile i was fetched
+  int issued = 0, st_in = 0;
+  auto issue = [&]() {
+    if (issued < n) {
+      if ((issued & 31) == 0 && issued > 0) {
+        rec_cur = rec_next;
+        if (issued + 32 < n) {
+          fc.forward(a, 32);
+          rec_next = record_of(issued + 32 + lane);
+        }
+      }
+      const int rec = __shfl_sync(0xffffffffu, rec_cur, issued & 31);
+      const uint32_t bit = 1u << (issued & 31);
+      if (rec >= 0) {
+        good |= bit;
+        const uint8_t* src = a.pool + (size_t)rec * C::REC + lane * 16;
+        const uint32_t dst = ring + st_in * C::REC + lane * 16;
+#pragma unroll
+        for (int i = 0; i < C::REC / 512; ++i) cp_async16(dst + i * 512, src + i * 512);
+        if constexpr (C::REC % 512 != 0) {
+          if (lane < (C::REC % 512) / 16) cp_async16(dst + C::REC / 512 * 512, src + C::REC / 512 * 512);
+        }
+      } else {
+        good &= ~bit;
+      }
+      ++issued;
+      st_in = st_in + 1 == C::STAGES ? 0 : st_in + 1;
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::STAGES - 1; ++i) issue();
+
+  // ---- the current segment
+  Kv4Cursor cc{f.x, f.y, f.z, 0};
+  int len = kv4_seq_len(a, cc.s);
+  cc.nt = (len + kKv4Tok - 1) / kKv4Tok;
+  bool cut = cc.t > 0;  // the segment began in an earlier warp's range
+  uint32_t qf[NT][NG * 4][2];   // B fragments of q, scaled per head
+  float qs[NT][NG][2];          // sum of the scaled q over a group, heads 2t and 2t + 1
+  float fac[NT][2];             // what turns the product with the scaled q into a log2 score
+  float m[NT][2], l[NT][2];     // reference of the exponentials, sum (this lane's tokens)
+  float zs[NT][NG][2];          // sum of p (m + 8 s) (this lane's tokens)
+  float oc[NT][NG * 4][4];      // O^T / 2^es: rows 8g + 2mt (+1), heads 2t, 2t + 1
+  int es[NG];                   // exponent the V scales of a group are divided by
+  int nrows = 0, hq0 = 0;
+
+  auto begin = [&]() {
+    const int kvh = cc.c / a.n_hg, hg = cc.c % a.n_hg;
+    hq0 = kvh * a.group + hg * C::ROWS;
+    nrows = min(C::ROWS, a.group - hg * C::ROWS);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool there = nt * 8 + g < nrows;
+      const __nv_bfloat16* qp = a.q + ((size_t)cc.s * a.Hq + hq0 + nt * 8 + g) * D + 16 * t;
+      uint2 raw[NG * 4];
+      float big = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < NG * 4; ++ks) {
+        raw[ks] = there ? __ldg(reinterpret_cast<const uint2*>(qp + (ks >> 2) * 64 + (ks & 3) * 4)) : make_uint2(0, 0);
+        big = fmaxf(big, fmaxf(fmaxf(fabsf(bf16lo_to_f32(raw[ks].x)), fabsf(bf16hi_to_f32(raw[ks].x))),
+                               fmaxf(fabsf(bf16lo_to_f32(raw[ks].y)), fabsf(bf16hi_to_f32(raw[ks].y)))));
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // largest element to [2^13, 2^14): fp16 then holds every element down to 2^-31 of it exactly
+      const int e = exponent_of(big, 127) - 13;
+      const float down = pow2i(-e);
+#pragma unroll
+      for (int ks = 0; ks < NG * 4; ++ks) {
+        qf[nt][ks][0] = pack_f16x2(bf16lo_to_f32(raw[ks].x) * down, bf16hi_to_f32(raw[ks].x) * down);
+        qf[nt][ks][1] = pack_f16x2(bf16lo_to_f32(raw[ks].y) * down, bf16hi_to_f32(raw[ks].y) * down);
+      }
+      // this lane's e belongs to head g; the fragments of the products want heads 2t and 2t + 1
+      fac[nt][0] = a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t));
+      fac[nt][1] = a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t + 4));
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_16816_f16(s4, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, qf[nt][4 * y + ks][0],
+                        qf[nt][4 * y + ks][1]);
+        qs[nt][y][0] = s4[0];
+        qs[nt][y][1] = s4[1];
+        zs[nt][y][0] = zs[nt][y][1] = 0.f;
+      }
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG * 4; ++i) oc[nt][i][0] = oc[nt][i][1] = oc[nt][i][2] = oc[nt][i][3] = 0.f;
+    }
+#pragma unroll
+    for (int y = 0; y < NG; ++y) es[y] = -100;
+  };
+  begin();
+
+  int st = 0;
+  for (int i = 0; i < n; ++i) {
+    cp_async_wait<C::STAGES - 2>();
+    __syncwarp();
+    const bool ok = (good >> (i & 31)) & 1u;  // read before issue() reuses the bit
+    issue();  // into the stage of tile i - 1, which every lane has left
+    if (ok) {
+      const uint32_t base = ring + st * C::REC;
+      // ---- S^T = (c - 8) q^T, scaled and shifted per group
+      uint32_t kp[2][NG], vp[2][NG];  // parameters of this lane's tokens: rows g and g + 8
+      {
+        uint32_t w[2 * NG >= 4 ? 4 : 2 * NG];
+        constexpr int PER = 2 * NG >= 4 ? 4 : 2 * NG;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int o = 0; o < 2 * NG; o += PER) {
+            lds_words<PER>(base + 1024 * NG + 64 * NG * v + (g * 2 * NG + o) * 4, w);
+#pragma unroll
+            for (int x = 0; x < PER; ++x) (v == 0 ? kp : vp)[(o + x) / NG][(o + x) % NG] = w[x];
+          }
+      }
+      float x[NT][4];  // scores: [row g: heads 2t, 2t+1][row g + 8: ...]
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+        const uint4 u = lds128(base + 512 * y + lane * 16);
+        uint32_t lo[2][4], hi[2][4];  // [word][pair] of rows g and g + 8
+        kv4_centred(u.x, lo[0]);
+        kv4_centred(u.y, lo[1]);
+        kv4_centred(u.z, hi[0]);
+        kv4_centred(u.w, hi[1]);
+        const float s0 = bf16lo_to_f32(kp[0][y]), s1 = bf16lo_to_f32(kp[1][y]);
+        const float z0 = fmaf(8.0f, s0, bf16hi_to_f32(kp[0][y])), z1 = fmaf(8.0f, s1, bf16hi_to_f32(kp[1][y]));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_16816_f16(c, lo[ks >> 1][2 * (ks & 1)], hi[ks >> 1][2 * (ks & 1)], lo[ks >> 1][2 * (ks & 1) + 1],
+                          hi[ks >> 1][2 * (ks & 1) + 1], qf[nt][4 * y + ks][0], qf[nt][4 * y + ks][1]);
+          if (y == 0) {
+            x[nt][0] = fmaf(s0, c[0], z0 * qs[nt][y][0]);
+            x[nt][1] = fmaf(s0, c[1], z0 * qs[nt][y][1]);
+            x[nt][2] = fmaf(s1, c[2], z1 * qs[nt][y][0]);
+            x[nt][3] = fmaf(s1, c[3], z1 * qs[nt][y][1]);
+          } else {
+            x[nt][0] = fmaf(s0, c[0], fmaf(z0, qs[nt][y][0], x[nt][0]));
+            x[nt][1] = fmaf(s0, c[1], fmaf(z0, qs[nt][y][1], x[nt][1]));
+            x[nt][2] = fmaf(s1, c[2], fmaf(z1, qs[nt][y][0], x[nt][2]));
+            x[nt][3] = fmaf(s1, c[3], fmaf(z1, qs[nt][y][1], x[nt][3]));
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        x[nt][0] *= fac[nt][0];
+        x[nt][1] *= fac[nt][1];
+        x[nt][2] *= fac[nt][0];
+        x[nt][3] *= fac[nt][1];
+      }
+      float vs[2][NG], vz[2][NG];
+#pragma unroll
+      for (int y = 0; y < NG; ++y)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          vs[r][y] = bf16lo_to_f32(vp[r][y]);
+          vz[r][y] = fmaf(8.0f, vs[r][y], bf16hi_to_f32(vp[r][y]));
+        }
+      if (cc.t == cc.nt - 1 && (len & 15) != 0) {
+        // tokens past the sequence's end: whatever the slot holds must not reach a sum
+        const int tok0 = cc.t * kKv4Tok + 4 * (g >> 1) + (g & 1);  // row g; row g + 8 is 2 tokens further
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (tok0 + 2 * r >= len) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[nt][2 * r] = x[nt][2 * r + 1] = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < NG; ++y) vs[r][y] = vz[r][y] = 0.f;
+          }
+      }
+      // ---- references: raised when a score passes m by 8, or a V scale 2^es by 2^6
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        raise |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + 8.0f || fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + 8.0f;
+#pragma unroll
+      for (int y = 0; y < NG; ++y) raise |= fmaxf(vs[0][y], vs[1][y]) > pow2i(es[y] + 6);
+      if (__any_sync(0xffffffffu, raise)) {
+        float down[NG];
+#pragma unroll
+        for (int y = 0; y < NG; ++y) {
+          const float big = max_over_rows(fmaxf(vs[0][y], vs[1][y]));
+          const int e = max(es[y], exponent_of(big, 120));
+          down[y] = pow2i(max(es[y] - e, -126));
+          es[y] = e;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float top = fmaxf(m[nt][hh], max_over_rows(fmaxf(x[nt][hh], x[nt][2 + hh])));
+            const float al = top == -INFINITY ? 1.0f : ex2(m[nt][hh] - top);
+            m[nt][hh] = top;
+            l[nt][hh] *= al;
+#pragma unroll
+            for (int y = 0; y < NG; ++y) {
+              zs[nt][y][hh] *= al;
+#pragma unroll
+              for (int mt = 0; mt < 4; ++mt) {
+                oc[nt][4 * y + mt][hh] *= al * down[y];
+                oc[nt][4 * y + mt][2 + hh] *= al * down[y];
+              }
+            }
+          }
+      }
+      // ---- P and the sums of its lane's tokens
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float u0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], u1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        x[nt][0] = ex2(x[nt][0] - u0);
+        x[nt][1] = ex2(x[nt][1] - u1);
+        x[nt][2] = ex2(x[nt][2] - u0);
+        x[nt][3] = ex2(x[nt][3] - u1);
+        l[nt][0] += x[nt][0] + x[nt][2];
+        l[nt][1] += x[nt][1] + x[nt][3];
+      }
+      // ---- O^T += (c - 8)^T (p s)^T
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+        const float unit = pow2i(-es[y]);
+        const float s0 = vs[0][y] * unit, s1 = vs[1][y] * unit;
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          b[nt][0] = movmatrix_trans(pack_f16x2(x[nt][0] * s0, x[nt][1] * s0));
+          b[nt][1] = movmatrix_trans(pack_f16x2(x[nt][2] * s1, x[nt][3] * s1));
+          zs[nt][y][0] = fmaf(x[nt][0], vz[0][y], fmaf(x[nt][2], vz[1][y], zs[nt][y][0]));
+          zs[nt][y][1] = fmaf(x[nt][1], vz[0][y], fmaf(x[nt][3], vz[1][y], zs[nt][y][1]));
+        }
+        const uint4 u = lds128(base + 512 * NG + 512 * y + 128 * t + 16 * (g ^ (2 * t)));
+        uint32_t p01[4], p23[4];  // tokens b = 0, 1 and b = 2, 3: channels c of a half of the unit
+        kv4_centred(u.x, p01);
+        kv4_centred(u.z, p23);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816_f16(oc[nt][4 * y + mt], p01[2 * mt], p01[2 * mt + 1], p23[2 * mt], p23[2 * mt + 1], b[nt][0],
+                          b[nt][1]);
+        kv4_centred(u.y, p01);
+        kv4_centred(u.w, p23);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816_f16(oc[nt][4 * y + 2 + mt], p01[2 * mt], p01[2 * mt + 1], p23[2 * mt], p23[2 * mt + 1],
+                          b[nt][0], b[nt][1]);
+      }
+    }
+    st = st + 1 == C::STAGES ? 0 : st + 1;
+
+    // ---- end of the segment, or of this warp's range
+    const bool end = cc.t == cc.nt - 1;
+    if (end || i == n - 1) {
+      const bool whole = end && !cut;
+      const size_t prow = (size_t)(wslot + (cut ? 0 : 1)) * C::ROWS;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float sum = sum_over_rows(l[nt][hh]);
+          const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // NaN stays
+          const float lse2 = sum != 0.0f ? m[nt][hh] + log2f(sum) : -INFINITY;
+          const int row = nt * 8 + 2 * t + hh;
+#pragma unroll
+          for (int y = 0; y < NG; ++y) {
+            const float z = sum_over_rows(zs[nt][y][hh]);
+            const float up = pow2i(es[y]);
+            float v[8];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              v[2 * mt] = fmaf(oc[nt][4 * y + mt][hh], up, z) * inv;
+              v[2 * mt + 1] = fmaf(oc[nt][4 * y + mt][2 + hh], up, z) * inv;
+            }
+            if (row < nrows) {
+              const int ch = 64 * y + 8 * g;
+              if (whole) {
+                *reinterpret_cast<uint4*>(a.o + ((size_t)cc.s * a.Hq + hq0 + row) * D + ch) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(a.part_o + (prow + row) * D + ch);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+              }
+            }
+          }
+          if (g == 0 && row < nrows) {
+            if (!whole)
+              a.part_lse[prow + row] = lse2;
+            else if (a.lse != nullptr)
+              a.lse[(size_t)cc.s * a.Hq + hq0 + row] = lse2 * 0.6931471805599453f;
+          }
+        }
+      if (i + 1 < n) {
+        cc.forward(a, 1);
+        len = kv4_seq_len(a, cc.s);
+        cut = false;
+        begin();
+      }
+    } else {
+      ++cc.t;
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------ merge kernel
+
+// One warp per (sequence, query head): joins the partials of a segment that more than one
+// warp's range shares; writes the rows of empty sequences.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) attn_decode_kv4_merge_kernel(const __grid_constant__ DecKv4Args a) {
+  using C = DecKv4Cfg<D, NT>;
+  const int wid = (int)((blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5);
+  const int lane = threadIdx.x & 31;
+  if (wid >= a.S * a.Hq) return;
+  const int s = wid / a.Hq, h = wid % a.Hq;
+  constexpr int PER = D / 32;
+  const long long p0 = a.tile_prefix[s], p1 = a.tile_prefix[s + 1], per = a.tile_prefix[a.S + 1];
+  const int nt = (int)(p1 - p0);
+  __nv_bfloat16* dst = a.o + ((size_t)s * a.Hq + h) * D + lane * PER;
+  float acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  float M = -INFINITY, L = 0.f;
+  if (nt > 0) {
+    const int in_kv = h % a.group;
+    const int c = (h / a.group) * a.n_hg + in_kv / C::ROWS;
+    const int row = in_kv % C::ROWS;
+    const long long f0 = p0 * (a.Hkv * a.n_hg) + (long long)c * nt, f1 = f0 + nt;
+    const long long w0 = f0 / per, w1 = (f1 - 1) / per;
+    if (w0 == w1) return;  // finished by the warp that had all of it
+    // the first warp's partial is the one it ended its range with (slot 1), the others' began before them
+    for (long long w = w0; w <= w1; ++w)
+      M = fmaxf(M, a.part_lse[(size_t)(2 * w + (w == w0 ? 1 : 0)) * C::ROWS + row]);
+    const float u = M == -INFINITY ? 0.f : M;
+    for (long long w = w0; w <= w1; ++w) {
+      const size_t pi = (size_t)(2 * w + (w == w0 ? 1 : 0)) * C::ROWS + row;
+      const float k = ex2(a.part_lse[pi] - u);
+      L += k;
+      const float* po = a.part_o + pi * D + lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(po + i);
+        acc[i] = fmaf(k, v.x, acc[i]);
+        acc[i + 1] = fmaf(k, v.y, acc[i + 1]);
+      }
+    }
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[(size_t)s * a.Hq + h] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+}  // namespace attn

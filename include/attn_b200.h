@@ -50,7 +50,8 @@ typedef enum attn_status {
   ATTN_ERR_WORKSPACE = 7,       /* workspace null or smaller than attn_decode_paged_workspace_size */
   ATTN_ERR_TOO_LARGE = 8        /* attn_decode_paged_noalloc: the call needs more scratch than the
                                    library's static scratch holds; attn_fwd_masked: Nk is past
-                                   the bound its block-sparse map allows */
+                                   the bound its block-sparse map allows; attn_pages_fork: the
+                                   rows need more pages than are free (latched on the device) */
 } attn_status;
 
 typedef enum attn_dtype {
@@ -285,6 +286,157 @@ attn_status attn_decode_paged_noalloc(const void* q, const void* k_pool, const v
 
 /* Size in bytes of the static scratch of attn_decode_paged_noalloc. */
 size_t attn_decode_paged_noalloc_max_scratch(void);
+
+/*
+ * The 4-bit paged cache.
+ *
+ * A cached key or value is held as x = s * c + m: a 4-bit code c and, per token and group of
+ * 64 channels, a bf16 scale s and a bf16 minimum m (d * 9/8 bytes per token and KV head for K and
+ * V together, against 4 * d in bf16).  For a group with smallest value `min` and largest `max`:
+ *     m = min (a zero as +0),  s = bf16((max - min) / 15) with the subtraction and the division
+ *     in fp32, c = the integer nearest to (x - m) / s, ties to even, at most 15.
+ * The quotient that decides c is taken exactly, not from a rounded fp32 division.  A group with an
+ * infinite or NaN value, or whose range overflows fp32, is stored as NaN (s = m = NaN).
+ *
+ * kv_pool: uint8 [num_pages, Hkv, page_size / 16, record], 16-byte aligned.  A record holds K and V
+ * of 16 consecutive tokens of one KV head in 1152 * NG bytes, NG = d / 64.  With token (within the
+ * record) = 4a + 2 b1 + b0 and channel = 64 y + x:
+ *     K codes      byte 512 y + 16 ((2a + b0) 4 + x/16) + 8 b1 + 4 ((x/8) % 2): a little-endian
+ *                  32-bit word of 8 channels; channel j = x % 8 in nibble j/2 + 4 (j % 2)
+ *     V codes      byte 512 NG + 512 y + 128 a + 16 ((x/8) ^ 2a) + 8 b1 + 4 ((x/4) % 2): a word of
+ *                  4 channels of 2 tokens; nibble 4 b0 + x % 4
+ *     parameters   byte 1024 NG (K) or 1088 NG (V) + 4 (((2a + b0) 2 + b1) NG + y): s in the low
+ *                  half of the word, m in the high half
+ * page_size is 16, 32 or 64 and d is 64, 128 or 256; num_pages * Hkv * page_size / 16 < 2^31.
+ */
+
+/* Bytes of one page of a 4-bit pool: Hkv * page_size * d * 9 / 8, or 0 for unsupported sizes. */
+size_t attn_kv4_page_bytes(int Hkv, int page_size, int d);
+
+/*
+ * attn_kv4_append — quantizes the K and V of new tokens into a 4-bit paged cache.
+ *
+ *   k, v         device, bf16 [num_new, Hkv, d], read-only, 16-byte aligned; consecutive tokens lie
+ *                k_stride (v_stride) elements apart, a multiple of 8 and at least Hkv * d, so that
+ *                slices of a fused projection's output can be passed as they are
+ *   kv_pool      device, the 4-bit pool (written: the new tokens' codes and parameters only)
+ *   block_table  device, int32 [num_seqs, max_pages_per_seq], as in attn_decode_paged
+ *   seq_lens     device, int32 [num_seqs]: length of each sequence WITH its new tokens
+ *   cu_new       device, int32 [num_seqs + 1], increasing from 0 to num_new: rows cu_new[s] ..
+ *                cu_new[s + 1] - 1 of k and v are the last tokens of sequence s
+ *   k_out, v_out device, bf16 [num_new, Hkv, d] (dense, 16-byte aligned) or NULL: written with the
+ *                values the cache now stands for, rounded to bf16, so that a prompt's own attention can
+ *                see exactly what later decode steps will see
+ * A slot must not be written by two tokens of one call (pages shared between rows are for reading:
+ * see attn_pages_fork).  A table entry in use outside [0, num_pages) is skipped and latches
+ * ATTN_ERR_BAD_PAGE; a sequence whose seq_lens or cu_new entries are out of range is skipped and
+ * latches ATTN_ERR_INVALID_ARG.  One kernel; nothing is allocated.
+ */
+attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, void* kv_pool,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_new,
+                            int page_size, void* k_out, void* v_out, int num_seqs, int num_new, int Hkv, int d,
+                            int num_pages, int max_pages_per_seq, void* stream);
+
+/*
+ * attn_kv4_gather — reads cached tokens back as bf16 K and V in attn_fwd's layout (for the next
+ * chunk of a prompt, whose queries attend to the whole cached context).
+ *
+ *   k, v         device, bf16 [num_seqs, Hkv, N, d], 16-byte aligned: tokens 0 .. min(seq_lens[s], N) - 1
+ *                of every sequence are written with the cached values rounded to bf16; rows past a
+ *                sequence's end are left as they were
+ * Other arguments as in attn_kv4_append.  Tokens of a table entry outside [0, num_pages) are skipped
+ * (ATTN_ERR_BAD_PAGE is latched), as is a sequence with a length outside
+ * [0, max_pages_per_seq * page_size] (ATTN_ERR_INVALID_ARG).
+ */
+attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, const int32_t* seq_lens,
+                            int page_size, void* k, void* v, int num_seqs, int Hkv, int N, int d, int num_pages,
+                            int max_pages_per_seq, void* stream);
+
+/*
+ * attn_decode_paged_kv4_workspace_size — bytes of scratch attn_decode_paged_kv4 needs on the
+ * current device (the work is split evenly over its SMs, so the size does not grow with the
+ * sequences' lengths).  0 for sizes the call would reject.
+ */
+size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d);
+
+/*
+ * attn_decode_paged_kv4 — attn_decode_paged over a 4-bit cache: o = softmax(scale q K^T) V with the
+ * cached values x = s * c + m.  The codes enter the matrix products exactly; scores, running maxima
+ * and sums are fp32, and the probabilities are rounded to 11 bits before P V.
+ *
+ *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned
+ *   lse          device, fp32 [num_seqs, Hq] or NULL
+ *   workspace    device scratch of at least attn_decode_paged_kv4_workspace_size(...) bytes, 256-byte
+ *                aligned, overwritten; two calls in flight at once need two workspaces
+ * Other arguments, empty sequences and bad pages as in attn_decode_paged.  A sequence length outside
+ * [0, max_pages_per_seq * page_size] counts as 0 and latches ATTN_ERR_INVALID_ARG.  What a page
+ * holds past its sequence's end is never used.  Two kernels, whose result does not depend on the
+ * order in which the GPU runs them.
+ */
+attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int32_t* block_table,
+                                  const int32_t* seq_lens, int page_size, void* o, float* lse, int num_seqs,
+                                  int Hq, int Hkv, int d, int num_pages, int max_pages_per_seq, float scale,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Pages of a cache (bf16 pools of attn_decode_paged or 4-bit pools).  The block table is the only
+ * state: a page is in use while some row refers to it among its first ceil(seq_lens / page_size)
+ * entries, and free otherwise.  Several pools (K and V, every layer) can share one table:
+ *
+ *   pools       HOST array of n_pools (0 .. 128) device pointers, 16-byte aligned, each to num_pages pages
+ *               of page_bytes bytes (a multiple of 16); copied during the call
+ *   page_size   tokens per page (any positive number)
+ *
+ * attn_pages_workspace_size — scratch of attn_pages_fork (rows = new_rows) and attn_pages_compact
+ * (rows = num_seqs): 256-byte aligned, needs no initialisation, one per call in flight.
+ */
+size_t attn_pages_workspace_size(int num_pages, int rows);
+
+/*
+ * attn_pages_fork — a new table whose rows continue rows of an old one: forks (a parent named by
+ * several rows), frees (a parent named by none), reorders, grows and truncates sequences.
+ *
+ *   block_table, seq_lens    device, int32 [num_seqs, max_pages_per_seq] and [num_seqs]: the old rows
+ *   parents     device, int32 [new_rows]: old row that new row i continues, or -1 for an empty row
+ *   add_tokens  device, int32 [new_rows] or NULL (zeros): new_lens[i] = seq_lens[parents[i]] + add_tokens[i];
+ *               a negative number drops the last tokens
+ *   new_table   device, int32 [new_rows, new_max_pages], new_max_pages >= max_pages_per_seq (written; -1 past
+ *               each row's pages); must not overlap block_table
+ *   new_lens    device, int32 [new_rows] (written); must not overlap the inputs
+ *   n_free      device, int32 [1] or NULL: pages left free
+ *
+ * Full pages are shared by the rows that continue them.  The part-filled page after a row's kept
+ * tokens will be written to, so it belongs to one row: the lowest row that has it keeps it in place
+ * unless a row has it as a full page, and every other row gets a copy of it (all pools, whole
+ * page) in a page from the free ones.  Entries for tokens beyond the kept ones are taken from the free
+ * pages too.  Free pages are those in no row of the new table; they are handed out in ascending
+ * order, row by row.  If they run out, the remaining entries are -1 and ATTN_ERR_TOO_LARGE is latched.
+ * A parent outside [-1, num_seqs) gives an empty row, a length that does not fit leaves the row's length
+ * unchanged (an old length out of range counts as 0), and a table entry in use outside [0, num_pages)
+ * becomes -1; these latch ATTN_ERR_INVALID_ARG, ATTN_ERR_INVALID_ARG and ATTN_ERR_BAD_PAGE.
+ */
+attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens, const int32_t* parents,
+                            const int32_t* add_tokens, int32_t* new_table, int32_t* new_lens, int page_size,
+                            void* const* pools, int n_pools, size_t page_bytes, int num_seqs,
+                            int max_pages_per_seq, int new_rows, int new_max_pages, int num_pages,
+                            int32_t* n_free, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_pages_compact — renumbers the n pages in use to 0 .. n-1 and moves their contents, so that the
+ * pool's tail is free: pages below n stay, the others go in ascending order to the free numbers below
+ * n, in ascending order.
+ *
+ *   new_table  device, int32 [num_seqs, max_pages_per_seq] (written; -1 past each row's pages); may be
+ *              block_table itself, must not overlap it otherwise
+ *   page_map   device, int32 [num_pages] (written): new number of each page, -1 where it was free
+ *   n_live     device, int32 [1] or NULL: n
+ * A length out of range counts as 0 and a table entry in use outside [0, num_pages) becomes -1; these
+ * latch ATTN_ERR_INVALID_ARG and ATTN_ERR_BAD_PAGE.
+ */
+attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_lens, int32_t* new_table,
+                               int32_t* page_map, int page_size, void* const* pools, int n_pools,
+                               size_t page_bytes, int num_seqs, int max_pages_per_seq, int num_pages,
+                               int32_t* n_live, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * attn_get_device_status — synchronises `stream`, then returns and clears the first

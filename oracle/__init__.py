@@ -17,3 +17,4 @@ from .attention import (  # noqa: F401
 )
 from .backward import attention_backward, attention_head_backward  # noqa: F401
 from .fp8 import attention_fp8_reference, block_quantize, dequantize, e4m3_value, quantize_e4m3  # noqa: F401
+from .kv4 import decode_paged_kv4  # noqa: F401
