@@ -37,6 +37,24 @@ attn_status launch_gather(const attn::Kv4GatherArgs& a, unsigned grid, cudaStrea
   return launch_status();
 }
 
+// Launches a kernel that may be set up while the kernel before it on the stream still runs; the
+// kernel waits for that one's results itself (pdl_wait).
+template <typename... P, typename... A>
+attn_status launch_dependent(void (*k)(P...), int grid, int threads, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...) == cudaSuccess ? launch_status() : ATTN_ERR_CUDA;
+}
+
 struct DecKv4Layout {
   size_t off_lse, off_o, total;
   long long warps;
@@ -49,7 +67,7 @@ int kv4_head_tiles(int group, int d) { return group > 8 && d <= 128 ? 2 : 1; }
 DecKv4Layout kv4_layout(int S, int group, int d) {
   DecKv4Layout L;
   const int nt = kv4_head_tiles(group, d);
-  L.warps = (long long)sm_count() * (d * nt <= 128 ? 4 : 2) * 4;
+  L.warps = (long long)sm_count() * (d * nt <= 64 ? 4 : (d * nt <= 128 ? 3 : 2)) * 4;
   L.off_lse = align256((size_t)(S + 2) * 8);
   L.off_o = L.off_lse + align256((size_t)L.warps * 2 * 8 * nt * 4);
   L.total = L.off_o + (size_t)L.warps * 2 * 8 * nt * d * 4;
@@ -62,14 +80,14 @@ attn_status launch_decode_kv4(const attn::DecKv4Args& a, cudaStream_t st, int sl
   auto k = attn::attn_decode_kv4_split_kernel<D, NT>;
   if (!ensure_smem(k, C::SMEM, slot)) return ATTN_ERR_CUDA;
   // no more CTAs than the longest possible rows can feed
-  const double ctas = std::ceil((double)a.S * a.max_pages * (1 << a.lg_blocks) * a.Hkv * a.n_hg /
-                                (C::WARPS * attn::kDecKv4MinTiles));
+  const double units = ((double)a.max_pages * a.page_size + attn::kDecKv4Unit - 1) / attn::kDecKv4Unit;
+  const double ctas = std::ceil(a.S * units * a.Hkv * a.n_hg / (C::WARPS * attn::kDecKv4MinUnits));
   const int grid = (int)std::max(1.0, std::min(ctas, (double)sm_count() * C::CTAS_PER_SM));
   k<<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  const long long rows = (long long)a.S * a.Hq;
-  attn::attn_decode_kv4_merge_kernel<D, NT><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
-  return launch_status();
+  if (a.S * a.Hq <= 4 * sm_count())
+    return launch_dependent(attn::attn_decode_kv4_merge_kernel<D, NT, 16>, a.S * a.Hq, 16 * 32, st, a);
+  return launch_dependent(attn::attn_decode_kv4_merge_kernel<D, NT, 4>, a.S * a.Hq, 4 * 32, st, a);
 }
 
 struct PagesLayout {
@@ -236,7 +254,7 @@ attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int3
   a.seq_lens = seq_lens;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  a.tile_prefix = reinterpret_cast<long long*>(ws);
+  a.unit_prefix = reinterpret_cast<long long*>(ws);
   a.part_lse = reinterpret_cast<float*>(ws + L.off_lse);
   a.part_o = reinterpret_cast<float*>(ws + L.off_o);
   a.S = num_seqs;

@@ -22,7 +22,7 @@
 //   * The running maximum is raised only when a score passes it by more than 2^8: one vote per
 //     16 tokens in place of six shuffles and a rescale.  P stays below 2^8 in between.
 //
-// Work split: the 16-token tiles of all (sequence, KV head, head group) segments form one
+// Work split: the 32-token units of all (sequence, KV head, head group) segments form one
 // stream; every warp takes an equal contiguous range of it, whatever the lengths, and runs alone: it
 // fetches its records with 16-byte asynchronous copies into its own ring in shared memory and
 // never waits for another warp.  A segment that lies inside one warp's range is finished there; the
@@ -40,7 +40,7 @@ struct DecKv4Args {
   const int32_t* seq_lens;     // [S]
   __nv_bfloat16* o;            // [S, Hq, d]
   float* lse;                  // [S, Hq] or null
-  long long* tile_prefix;      // workspace: [S + 1] tiles of the sequences before s, then the range length
+  long long* unit_prefix;      // workspace: [S + 1] units of the sequences before s, then the range length
   float* part_o;               // workspace: [warps][2][8 NT][d]
   float* part_lse;             // workspace: [warps][2][8 NT], log2 units
   int S, Hq, Hkv, group, n_hg, page_size, lg_blocks, num_pages, max_pages;
@@ -52,14 +52,17 @@ struct DecKv4Cfg {
   static constexpr int NG = D / kKv4Group;
   static constexpr int ROWS = 8 * NT;  // query heads of a segment
   static constexpr int REC = kv4_record_bytes(D);
+  static constexpr int UNIT = 2 * REC;  // a unit of work: 32 tokens, two records
   static constexpr int WARPS = 4;
-  static constexpr int CTAS_PER_SM = (D * NT <= 128) ? 4 : 2;
-  static constexpr int STAGES = (D == 64) ? 8 : 6;
-  static constexpr int SMEM = WARPS * STAGES * REC;
+  // resident CTAs: as many as the registers of the accumulators leave room for
+  static constexpr int CTAS_PER_SM = D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : 2);
+  static constexpr int STAGES = (D == 64) ? 4 : 3;
+  static constexpr int SMEM = WARPS * STAGES * UNIT;
   static constexpr int THREADS = WARPS * 32;
 };
 
-constexpr int kDecKv4MinTiles = 4;  // shortest range of a warp: 64 tokens
+constexpr int kDecKv4Unit = 2 * kKv4Tok;  // tokens of a unit
+constexpr int kDecKv4MinUnits = 2;        // shortest range of a warp: 64 tokens
 
 // ------------------------------------------------------------------ fp16 and copy helpers
 
@@ -72,6 +75,30 @@ __device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+// c = a b, the first step of a product.
+__device__ __forceinline__ void mma_16816_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// a b + c with bf16 a and b (16-bit halves of a parameter word, say) and fp32 c: one FMA, where
+// widening a half first would cost an instruction of the half-rate integer pipe.
+__device__ __forceinline__ float fma_bf16(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"((uint16_t)a), "h"((uint16_t)b), "f"(c));
+  return d;
+}
+constexpr uint32_t kBf16One = 0x3f80u, kBf16Eight = 0x4100u;
+
+// Programmatic dependent launch: the dependent grid may be set up from here on; it waits for this
+// grid's end (and its writes) in pdl_wait.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Transposes an 8x8 matrix of 16-bit elements held by the warp (two neighbours of a row a lane).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -105,6 +132,29 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                  : "r"(addr));
   }
+}
+
+// The parameter words [row g, row g + 8][group] of a lane's two tokens.
+template <int NG>
+__device__ __forceinline__ void lds_params(uint32_t addr, uint32_t (&p)[2 * NG]) {
+  constexpr int PER = 2 * NG >= 4 ? 4 : 2 * NG;
+#pragma unroll
+  for (int o = 0; o < 2 * NG; o += PER) {
+    uint32_t w[PER];
+    lds_words<PER>(addr + o * 4, w);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) p[o + j] = w[j];
+  }
+}
+
+__device__ __forceinline__ void sts_word(uint32_t addr, uint32_t w) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -156,7 +206,12 @@ __device__ __forceinline__ int kv4_seq_len(const DecKv4Args& a, int s) {  // 0 f
   return len < 0 || len > a.max_pages * a.page_size ? 0 : len;
 }
 
-// A position in the stream: tile t of segment c (KV head and head group) of sequence s.
+// Units of sequence s.
+__device__ __forceinline__ int kv4_units(const DecKv4Args& a, int s) {
+  return (kv4_seq_len(a, s) + kDecKv4Unit - 1) / kDecKv4Unit;
+}
+
+// A position in the stream: unit t of segment c (KV head and head group) of sequence s.
 struct Kv4Cursor {
   int s, c, t, nt;
   __device__ __forceinline__ void forward(const DecKv4Args& a, int n) {
@@ -166,15 +221,15 @@ struct Kv4Cursor {
       if (++c == a.Hkv * a.n_hg) {
         c = 0;
         nt = 0;
-        while (++s < a.S && nt == 0) nt = (kv4_seq_len(a, s) + kKv4Tok - 1) / kKv4Tok;
+        while (++s < a.S && nt == 0) nt = kv4_units(a, s);
         if (nt > 0) --s;  // the loop's last increment passed the sequence found
       }
     }
   }
 };
 
-// Finds the first tiles of this CTA's warps: first[w] = {s, c, t, tiles of the range} (0 tiles: no
-// work).  Every thread of the block calls it.  CTA 0 also leaves the tile prefix for the merge.
+// Finds the first units of this CTA's warps: first[w] = {s, c, t, units of the range} (0 units: no
+// work).  Every thread of the block calls it.  CTA 0 also leaves the unit prefix for the merge.
 template <int WARPS>
 __device__ __forceinline__ void kv4_plan(const DecKv4Args& a, int4* first, long long* warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -183,7 +238,7 @@ __device__ __forceinline__ void kv4_plan(const DecKv4Args& a, int4* first, long 
   const int s0 = min(a.S, tid * per_thread), s1 = min(a.S, s0 + per_thread);
   long long mine = 0;
   for (int s = s0; s < s1; ++s) {
-    mine += (kv4_seq_len(a, s) + kKv4Tok - 1) / kKv4Tok;
+    mine += kv4_units(a, s);
     if (blockIdx.x == 0 && (__ldg(&a.seq_lens[s]) < 0 || __ldg(&a.seq_lens[s]) > a.max_pages * a.page_size))
       latch_status(ATTN_ERR_INVALID_ARG);
   }
@@ -203,10 +258,10 @@ __device__ __forceinline__ void kv4_plan(const DecKv4Args& a, int4* first, long 
     total += warp_sums[w];
   }
   const long long T = total * C, warps = (long long)gridDim.x * WARPS;
-  const long long per = max((T + warps - 1) / warps, (long long)kDecKv4MinTiles);
+  const long long per = max((T + warps - 1) / warps, (long long)kDecKv4MinUnits);
   for (int s = s0; s < s1; ++s) {
-    const int nt = (kv4_seq_len(a, s) + kKv4Tok - 1) / kKv4Tok;
-    if (blockIdx.x == 0) a.tile_prefix[s] = before;
+    const int nt = kv4_units(a, s);
+    if (blockIdx.x == 0) a.unit_prefix[s] = before;
     const long long f0 = before * C, f1 = f0 + (long long)nt * C;
     for (int w = 0; w < WARPS; ++w) {
       const long long f = ((long long)blockIdx.x * WARPS + w) * per;
@@ -216,8 +271,8 @@ __device__ __forceinline__ void kv4_plan(const DecKv4Args& a, int4* first, long 
     before += nt;
   }
   if (blockIdx.x == 0 && tid == 0) {
-    a.tile_prefix[a.S] = total;
-    a.tile_prefix[a.S + 1] = per;
+    a.unit_prefix[a.S] = total;
+    a.unit_prefix[a.S + 1] = per;
   }
   __syncthreads();
 }
@@ -235,98 +290,102 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;  // row and column pair of the MMA fragments
   kv4_plan<C::WARPS>(a, first, warp_sums);
+  pdl_launch_dependents();
   const int4 f = first[warp];
   const int n = f.w;
   if (n == 0) return;
-  const int wslot = 2 * (blockIdx.x * C::WARPS + warp);
-  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::REC);
+  const int wid = blockIdx.x * C::WARPS + warp;
+  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::UNIT);
 
-  // ---- fetch side: lane l keeps the record number of tile l of the current batch of 32 tiles
-  // (-1: its page is out of range), and of the next batch, whose table loads are then in flight
-  // long before they are needed
+  // ---- fetch side: lane l keeps the record number of tile l % 2 of unit l / 2 of the current
+  // batch of 16 units (-1: past the row's end, or its page is out of range), and of the next
+  // batch, whose table loads are then in flight long before they are needed
   Kv4Cursor fc{f.x, f.y, f.z, 0};
-  fc.nt = (kv4_seq_len(a, fc.s) + kKv4Tok - 1) / kKv4Tok;
-  fc.forward(a, lane);
-  auto record_of = [&](int tile) -> int {
-    if (tile >= n || fc.s >= a.S) return -1;
-    const int page = __ldg(&a.block_table[(size_t)fc.s * a.max_pages + (fc.t >> a.lg_blocks)]);
+  fc.nt = kv4_units(a, fc.s);
+  fc.forward(a, lane >> 1);
+  auto record_of = [&](int unit) -> int {
+    if (unit >= n || fc.s >= a.S) return -1;
+    const int tile = 2 * fc.t + (lane & 1);
+    if (tile * kKv4Tok >= kv4_seq_len(a, fc.s)) return -1;
+    const int page = __ldg(&a.block_table[(size_t)fc.s * a.max_pages + (tile >> a.lg_blocks)]);
     if (page < 0 || page >= a.num_pages) {
       latch_status(ATTN_ERR_BAD_PAGE);
       return -1;
     }
-    const int kvh = fc.c / a.n_hg;
-    return ((page * a.Hkv + kvh) << a.lg_blocks) + (fc.t & ((1 << a.lg_blocks) - 1));
+    return ((page * a.Hkv + fc.c / a.n_hg) << a.lg_blocks) + (tile & ((1 << a.lg_blocks) - 1));
   };
-  int rec_cur = record_of(lane);
-  fc.forward(a, 32);
-  int rec_next = n > 32 ? record_of(lane + 32) : -1;
-  uint32_t good = 0;  // bit i % 32: tile i was fetched
-  int issued = 0, st_in = 0;
-  auto issue = [&]() {
+  int rec_cur = record_of(lane >> 1);
+  int rec_next = -1;
+  if (n > 16) {
+    fc.forward(a, 16);
+    rec_next = record_of(16 + (lane >> 1));
+  }
+  uint32_t good = 0;  // bits 2 (i % 16) + tile: fetched
+  auto issue = [&](int issued, uint32_t in) {
     if (issued < n) {
-      if ((issued & 31) == 0 && issued > 0) {
+      if ((issued & 15) == 0 && issued > 0) {
         rec_cur = rec_next;
-        if (issued + 32 < n) {
-          fc.forward(a, 32);
-          rec_next = record_of(issued + 32 + lane);
+        if (issued + 16 < n) {
+          fc.forward(a, 16);
+          rec_next = record_of(issued + 16 + (lane >> 1));
         }
       }
-      const int rec = __shfl_sync(0xffffffffu, rec_cur, issued & 31);
-      const uint32_t bit = 1u << (issued & 31);
-      if (rec >= 0) {
-        good |= bit;
-        const uint8_t* src = a.pool + (size_t)rec * C::REC + lane * 16;
-        const uint32_t dst = ring + st_in * C::REC + lane * 16;
+      const int b = 2 * (issued & 15);
+      const int r0 = __shfl_sync(0xffffffffu, rec_cur, b), r1 = __shfl_sync(0xffffffffu, rec_cur, b + 1);
+      good = (good & ~(3u << b)) | ((r0 >= 0 ? 1u : 0u) << b) | ((r1 >= 0 ? 2u : 0u) << b);
 #pragma unroll
-        for (int i = 0; i < C::REC / 512; ++i) cp_async16(dst + i * 512, src + i * 512);
-        if constexpr (C::REC % 512 != 0) {
-          if (lane < (C::REC % 512) / 16) cp_async16(dst + C::REC / 512 * 512, src + C::REC / 512 * 512);
+      for (int x = 0; x < 2; ++x) {
+        const int rec = x == 0 ? r0 : r1;
+        if (rec >= 0) {
+          const uint8_t* src = a.pool + (size_t)rec * C::REC + lane * 16;
+          const uint32_t dst = in + x * C::REC + lane * 16;
+#pragma unroll
+          for (int i = 0; i < C::REC / 512; ++i) cp_async16(dst + i * 512, src + i * 512);
+          if constexpr (C::REC % 512 != 0) {
+            if (lane < (C::REC % 512) / 16) cp_async16(dst + C::REC / 512 * 512, src + C::REC / 512 * 512);
+          }
         }
-      } else {
-        good &= ~bit;
       }
-      ++issued;
-      st_in = st_in + 1 == C::STAGES ? 0 : st_in + 1;
     }
     cp_async_commit();
   };
 #pragma unroll 1
-  for (int i = 0; i < C::STAGES - 1; ++i) issue();
+  for (int i = 0; i < C::STAGES - 1; ++i) issue(i, ring + i * C::UNIT);
 
   // ---- the current segment
-  Kv4Cursor cc{f.x, f.y, f.z, 0};
-  int len = kv4_seq_len(a, cc.s);
-  cc.nt = (len + kKv4Tok - 1) / kKv4Tok;
-  bool cut = cc.t > 0;  // the segment began in an earlier warp's range
+  int cs = f.x, cc = f.y;  // sequence, and KV head and head group
+  int left = kv4_seq_len(a, cs) - f.z * kDecKv4Unit;  // tokens of the row from the current unit on
+  bool cut = f.z > 0;      // the segment began in an earlier warp's range
   uint32_t qf[NT][NG * 4][2];   // B fragments of q, scaled per head
   float qs[NT][NG][2];          // sum of the scaled q over a group, heads 2t and 2t + 1
   float fac[NT][2];             // what turns the product with the scaled q into a log2 score
-  float m[NT][2], l[NT][2];     // reference of the exponentials, sum (this lane's tokens)
+  float m[NT][2];               // reference of the exponentials (log2 score)
+  float l[NT][2];               // sum of exponentials (this lane's tokens)
   float zs[NT][NG][2];          // sum of p (m + 8 s) (this lane's tokens)
   float oc[NT][NG * 4][4];      // O^T / 2^es: rows 8g + 2mt (+1), heads 2t, 2t + 1
-  int es[NG];                   // exponent the V scales of a group are divided by
-  int nrows = 0, hq0 = 0;
-
+  float unit[NG];               // 2^-es, what the V scales of a group are multiplied by
+  auto head_of = [&](int c) -> int { return c / a.n_hg * a.group + c % a.n_hg * C::ROWS; };
+  auto rows_of = [&](int c) -> int { return min(C::ROWS, a.group - c % a.n_hg * C::ROWS); };
   auto begin = [&]() {
-    const int kvh = cc.c / a.n_hg, hg = cc.c % a.n_hg;
-    hq0 = kvh * a.group + hg * C::ROWS;
-    nrows = min(C::ROWS, a.group - hg * C::ROWS);
+    const int nrows = rows_of(cc), hq0 = head_of(cc);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool there = nt * 8 + g < nrows;
-      const __nv_bfloat16* qp = a.q + ((size_t)cc.s * a.Hq + hq0 + nt * 8 + g) * D + 16 * t;
       uint2 raw[NG * 4];
-      float big = 0.0f;
+      uint32_t big = 0;  // magnitudes of bf16 values order like their bits
 #pragma unroll
       for (int ks = 0; ks < NG * 4; ++ks) {
-        raw[ks] = there ? __ldg(reinterpret_cast<const uint2*>(qp + (ks >> 2) * 64 + (ks & 3) * 4)) : make_uint2(0, 0);
-        big = fmaxf(big, fmaxf(fmaxf(fabsf(bf16lo_to_f32(raw[ks].x)), fabsf(bf16hi_to_f32(raw[ks].x))),
-                               fmaxf(fabsf(bf16lo_to_f32(raw[ks].y)), fabsf(bf16hi_to_f32(raw[ks].y)))));
+        // channels 64 y + 16 t + 4 (ks % 4) .. of head g
+        raw[ks] = nt * 8 + g < nrows
+                      ? __ldg(reinterpret_cast<const uint2*>(a.q + ((size_t)cs * a.Hq + hq0 + nt * 8 + g) * D +
+                                                             16 * t + (ks >> 2) * 64 + (ks & 3) * 4))
+                      : make_uint2(0, 0);
+        big = max(big, max((raw[ks].x << 16) & 0x7fff0000u, raw[ks].x & 0x7fff0000u));
+        big = max(big, max((raw[ks].y << 16) & 0x7fff0000u, raw[ks].y & 0x7fff0000u));
       }
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
       // largest element to [2^13, 2^14): fp16 then holds every element down to 2^-31 of it exactly
-      const int e = exponent_of(big, 127) - 13;
+      const int e = exponent_of(__uint_as_float(big), 127) - 13;
       const float down = pow2i(-e);
 #pragma unroll
       for (int ks = 0; ks < NG * 4; ++ks) {
@@ -338,9 +397,10 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
       fac[nt][1] = a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t + 4));
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        float s4[4];
+        mma_16816_f16_first(s4, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, qf[nt][4 * y][0], qf[nt][4 * y][1]);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 1; ks < 4; ++ks)
           mma_16816_f16(s4, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, qf[nt][4 * y + ks][0],
                         qf[nt][4 * y + ks][1]);
         qs[nt][y][0] = s4[0];
@@ -353,33 +413,31 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
       for (int i = 0; i < NG * 4; ++i) oc[nt][i][0] = oc[nt][i][1] = oc[nt][i][2] = oc[nt][i][3] = 0.f;
     }
 #pragma unroll
-    for (int y = 0; y < NG; ++y) es[y] = -100;
+    for (int y = 0; y < NG; ++y) unit[y] = pow2i(100);
   };
   begin();
 
-  int st = 0;
+  uint32_t out = ring;
   for (int i = 0; i < n; ++i) {
     cp_async_wait<C::STAGES - 2>();
     __syncwarp();
-    const bool ok = (good >> (i & 31)) & 1u;  // read before issue() reuses the bit
-    issue();  // into the stage of tile i - 1, which every lane has left
-    if (ok) {
-      const uint32_t base = ring + st * C::REC;
-      // ---- S^T = (c - 8) q^T, scaled and shifted per group
-      uint32_t kp[2][NG], vp[2][NG];  // parameters of this lane's tokens: rows g and g + 8
-      {
-        uint32_t w[2 * NG >= 4 ? 4 : 2 * NG];
-        constexpr int PER = 2 * NG >= 4 ? 4 : 2 * NG;
+    const uint32_t have = (good >> (2 * (i & 15))) & 3u;  // read before issue() reuses the bits
+    // into the stage of unit i - 1, which every lane has left
+    issue(i + C::STAGES - 1, out == ring ? ring + (C::STAGES - 1) * C::UNIT : out - C::UNIT);
+    // ---- S^T = (c - 8) q^T of both tiles, scaled and shifted per group
+    float x[2][NT][4];       // products: [tile][..][row g: heads 2t, 2t+1; row g + 8: ...]
+    uint32_t smax[NG];       // the largest of this lane's V scales, as bf16 bits in the low half
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
+    for (int tile = 0; tile < 2; ++tile) {
+      const uint32_t base = out + tile * C::REC;
+      uint32_t kp[2 * NG], vp[2 * NG];  // parameters of this lane's tokens: [row g, g + 8][group]
+      lds_params<NG>(base + 1024 * NG + g * 8 * NG, kp);
+      lds_params<NG>(base + 1088 * NG + g * 8 * NG, vp);
 #pragma unroll
-          for (int o = 0; o < 2 * NG; o += PER) {
-            lds_words<PER>(base + 1024 * NG + 64 * NG * v + (g * 2 * NG + o) * 4, w);
-#pragma unroll
-            for (int x = 0; x < PER; ++x) (v == 0 ? kp : vp)[(o + x) / NG][(o + x) % NG] = w[x];
-          }
+      for (int y = 0; y < NG; ++y) {
+        const uint32_t w = max_u16x2(vp[y], vp[NG + y]);
+        smax[y] = tile == 0 ? w : max_u16x2(smax[y], w);
       }
-      float x[NT][4];  // scores: [row g: heads 2t, 2t+1][row g + 8: ...]
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         const uint4 u = lds128(base + 512 * y + lane * 16);
@@ -388,113 +446,128 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
         kv4_centred(u.y, lo[1]);
         kv4_centred(u.z, hi[0]);
         kv4_centred(u.w, hi[1]);
-        const float s0 = bf16lo_to_f32(kp[0][y]), s1 = bf16lo_to_f32(kp[1][y]);
-        const float z0 = fmaf(8.0f, s0, bf16hi_to_f32(kp[0][y])), z1 = fmaf(8.0f, s1, bf16hi_to_f32(kp[1][y]));
+        const float s0 = fma_bf16(kp[y], kBf16One, 0.f), s1 = fma_bf16(kp[NG + y], kBf16One, 0.f);
+        const float z0 = fma_bf16(kp[y], kBf16Eight, fma_bf16(kp[y] >> 16, kBf16One, 0.f));
+        const float z1 = fma_bf16(kp[NG + y], kBf16Eight, fma_bf16(kp[NG + y] >> 16, kBf16One, 0.f));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          float c[4];
+          float* xx = x[tile][nt];
+          mma_16816_f16_first(c, lo[0][0], hi[0][0], lo[0][1], hi[0][1], qf[nt][4 * y][0], qf[nt][4 * y][1]);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+          for (int ks = 1; ks < 4; ++ks)
             mma_16816_f16(c, lo[ks >> 1][2 * (ks & 1)], hi[ks >> 1][2 * (ks & 1)], lo[ks >> 1][2 * (ks & 1) + 1],
                           hi[ks >> 1][2 * (ks & 1) + 1], qf[nt][4 * y + ks][0], qf[nt][4 * y + ks][1]);
           if (y == 0) {
-            x[nt][0] = fmaf(s0, c[0], z0 * qs[nt][y][0]);
-            x[nt][1] = fmaf(s0, c[1], z0 * qs[nt][y][1]);
-            x[nt][2] = fmaf(s1, c[2], z1 * qs[nt][y][0]);
-            x[nt][3] = fmaf(s1, c[3], z1 * qs[nt][y][1]);
+            xx[0] = fmaf(s0, c[0], z0 * qs[nt][y][0]);
+            xx[1] = fmaf(s0, c[1], z0 * qs[nt][y][1]);
+            xx[2] = fmaf(s1, c[2], z1 * qs[nt][y][0]);
+            xx[3] = fmaf(s1, c[3], z1 * qs[nt][y][1]);
           } else {
-            x[nt][0] = fmaf(s0, c[0], fmaf(z0, qs[nt][y][0], x[nt][0]));
-            x[nt][1] = fmaf(s0, c[1], fmaf(z0, qs[nt][y][1], x[nt][1]));
-            x[nt][2] = fmaf(s1, c[2], fmaf(z1, qs[nt][y][0], x[nt][2]));
-            x[nt][3] = fmaf(s1, c[3], fmaf(z1, qs[nt][y][1], x[nt][3]));
+            xx[0] = fmaf(s0, c[0], fmaf(z0, qs[nt][y][0], xx[0]));
+            xx[1] = fmaf(s0, c[1], fmaf(z0, qs[nt][y][1], xx[1]));
+            xx[2] = fmaf(s1, c[2], fmaf(z1, qs[nt][y][0], xx[2]));
+            xx[3] = fmaf(s1, c[3], fmaf(z1, qs[nt][y][1], xx[3]));
           }
         }
       }
+    }
+    if (left < kDecKv4Unit || have != 3u) {
+      // tokens past the row's end or on a page out of range: whatever their slots hold must
+      // not reach a sum.  This lane's rows are tokens 4 (g/2) + g%2 and two further.
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] *= fac[nt][0];
-        x[nt][1] *= fac[nt][1];
-        x[nt][2] *= fac[nt][0];
-        x[nt][3] *= fac[nt][1];
-      }
-      float vs[2][NG], vz[2][NG];
-#pragma unroll
-      for (int y = 0; y < NG; ++y)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          vs[r][y] = bf16lo_to_f32(vp[r][y]);
-          vz[r][y] = fmaf(8.0f, vs[r][y], bf16hi_to_f32(vp[r][y]));
-        }
-      if (cc.t == cc.nt - 1 && (len & 15) != 0) {
-        // tokens past the sequence's end: whatever the slot holds must not reach a sum
-        const int tok0 = cc.t * kKv4Tok + 4 * (g >> 1) + (g & 1);  // row g; row g + 8 is 2 tokens further
+      for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (tok0 + 2 * r >= len) {
+          if (tile * kKv4Tok + 4 * (g >> 1) + (g & 1) + 2 * r >= left || !((have >> tile) & 1u)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[nt][2 * r] = x[nt][2 * r + 1] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) x[tile][nt][2 * r] = x[tile][nt][2 * r + 1] = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < NG; ++y) vs[r][y] = vz[r][y] = 0.f;
+            for (int y = 0; y < NG; ++y) sts_word(out + tile * C::REC + 1088 * NG + ((2 * g + r) * NG + y) * 4, 0u);
           }
+      __syncwarp();
+    }
+    // ---- references: raised when a score passes m by 8, or a V scale 2^es by 2^6 (scales are not
+    // negative, so their bits order like the values; a masked slot may only cause a needless look)
+    bool raise = false;
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        top[nt][hh] = fmaxf(fmaxf(x[0][nt][hh], x[0][nt][2 + hh]), fmaxf(x[1][nt][hh], x[1][nt][2 + hh]));
+        raise |= fmaf(top[nt][hh], fac[nt][hh], -m[nt][hh]) > 8.0f;
       }
-      // ---- references: raised when a score passes m by 8, or a V scale 2^es by 2^6
-      bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        raise |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + 8.0f || fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + 8.0f;
-#pragma unroll
-      for (int y = 0; y < NG; ++y) raise |= fmaxf(vs[0][y], vs[1][y]) > pow2i(es[y] + 6);
-      if (__any_sync(0xffffffffu, raise)) {
-        float down[NG];
-#pragma unroll
-        for (int y = 0; y < NG; ++y) {
-          const float big = max_over_rows(fmaxf(vs[0][y], vs[1][y]));
-          const int e = max(es[y], exponent_of(big, 120));
-          down[y] = pow2i(max(es[y] - e, -126));
-          es[y] = e;
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float top = fmaxf(m[nt][hh], max_over_rows(fmaxf(x[nt][hh], x[nt][2 + hh])));
-            const float al = top == -INFINITY ? 1.0f : ex2(m[nt][hh] - top);
-            m[nt][hh] = top;
-            l[nt][hh] *= al;
-#pragma unroll
-            for (int y = 0; y < NG; ++y) {
-              zs[nt][y][hh] *= al;
-#pragma unroll
-              for (int mt = 0; mt < 4; ++mt) {
-                oc[nt][4 * y + mt][hh] *= al * down[y];
-                oc[nt][4 * y + mt][2 + hh] *= al * down[y];
-              }
-            }
-          }
-      }
-      // ---- P and the sums of its lane's tokens
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float u0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], u1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-        x[nt][0] = ex2(x[nt][0] - u0);
-        x[nt][1] = ex2(x[nt][1] - u1);
-        x[nt][2] = ex2(x[nt][2] - u0);
-        x[nt][3] = ex2(x[nt][3] - u1);
-        l[nt][0] += x[nt][0] + x[nt][2];
-        l[nt][1] += x[nt][1] + x[nt][3];
-      }
-      // ---- O^T += (c - 8)^T (p s)^T
+    for (int y = 0; y < NG; ++y) raise |= fma_bf16(smax[y], __float_as_uint(unit[y]) >> 16, 0.f) > 64.0f;
+    if (__any_sync(0xffffffffu, raise)) {
+      float down[NG];
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
-        const float unit = pow2i(-es[y]);
-        const float s0 = vs[0][y] * unit, s1 = vs[1][y] * unit;
+        float big = 0.f;
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          uint32_t vp[2 * NG];
+          lds_params<NG>(out + tile * C::REC + 1088 * NG + g * 8 * NG, vp);
+          big = fmaxf(big, fmaxf(bf16lo_to_f32(vp[y]), bf16lo_to_f32(vp[NG + y])));
+        }
+        const int es = 127 - (int)((__float_as_uint(unit[y]) >> 23) & 0xffu);
+        const int to = max(es, exponent_of(max_over_rows(big), 120));
+        down[y] = pow2i(max(es - to, -126));
+        unit[y] = pow2i(-to);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float to = fmaxf(m[nt][hh], max_over_rows(top[nt][hh]) * fac[nt][hh]);
+          const float al = to == -INFINITY ? 1.0f : ex2(m[nt][hh] - to);
+          m[nt][hh] = to;
+          l[nt][hh] *= al;
+#pragma unroll
+          for (int y = 0; y < NG; ++y) {
+            zs[nt][y][hh] *= al;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              oc[nt][4 * y + mt][hh] *= al * down[y];
+              oc[nt][4 * y + mt][2 + hh] *= al * down[y];
+            }
+          }
+        }
+    }
+    // ---- P and the sums of its lane's tokens
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const float u = m[nt][hh] == -INFINITY ? 0.f : m[nt][hh];
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          x[tile][nt][hh] = ex2(fmaf(x[tile][nt][hh], fac[nt][hh], -u));
+          x[tile][nt][2 + hh] = ex2(fmaf(x[tile][nt][2 + hh], fac[nt][hh], -u));
+        }
+        l[nt][hh] += (x[0][nt][hh] + x[0][nt][2 + hh]) + (x[1][nt][hh] + x[1][nt][2 + hh]);
+      }
+    // ---- O^T += (c - 8)^T (p s)^T
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      const uint32_t base = out + tile * C::REC;
+      uint32_t vp[2 * NG];
+      lds_params<NG>(base + 1088 * NG + g * 8 * NG, vp);
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+        const uint32_t w0 = vp[y], w1 = vp[NG + y], by = __float_as_uint(unit[y]) >> 16;
+        const float s0 = fma_bf16(w0, by, 0.f), s1 = fma_bf16(w1, by, 0.f);
+        const float z0 = fma_bf16(w0, kBf16Eight, fma_bf16(w0 >> 16, kBf16One, 0.f));
+        const float z1 = fma_bf16(w1, kBf16Eight, fma_bf16(w1 >> 16, kBf16One, 0.f));
         uint32_t b[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          b[nt][0] = movmatrix_trans(pack_f16x2(x[nt][0] * s0, x[nt][1] * s0));
-          b[nt][1] = movmatrix_trans(pack_f16x2(x[nt][2] * s1, x[nt][3] * s1));
-          zs[nt][y][0] = fmaf(x[nt][0], vz[0][y], fmaf(x[nt][2], vz[1][y], zs[nt][y][0]));
-          zs[nt][y][1] = fmaf(x[nt][1], vz[0][y], fmaf(x[nt][3], vz[1][y], zs[nt][y][1]));
+          const float* p = x[tile][nt];
+          b[nt][0] = movmatrix_trans(pack_f16x2(p[0] * s0, p[1] * s0));
+          b[nt][1] = movmatrix_trans(pack_f16x2(p[2] * s1, p[3] * s1));
+          zs[nt][y][0] = fmaf(p[0], z0, fmaf(p[2], z1, zs[nt][y][0]));
+          zs[nt][y][1] = fmaf(p[1], z0, fmaf(p[3], z1, zs[nt][y][1]));
         }
         const uint4 u = lds128(base + 512 * NG + 512 * y + 128 * t + 16 * (g ^ (2 * t)));
         uint32_t p01[4], p23[4];  // tokens b = 0, 1 and b = 2, 3: channels c of a half of the unit
@@ -516,13 +589,15 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
                           b[nt][0], b[nt][1]);
       }
     }
-    st = st + 1 == C::STAGES ? 0 : st + 1;
+    out = out + C::UNIT == ring + C::STAGES * C::UNIT ? ring : out + C::UNIT;
 
     // ---- end of the segment, or of this warp's range
-    const bool end = cc.t == cc.nt - 1;
+    const bool end = left <= kDecKv4Unit;
+    left -= kDecKv4Unit;
     if (end || i == n - 1) {
       const bool whole = end && !cut;
-      const size_t prow = (size_t)(wslot + (cut ? 0 : 1)) * C::ROWS;
+      const int nrows = rows_of(cc), hq0 = head_of(cc);
+      const size_t prow = (size_t)(2 * wid + (cut ? 0 : 1)) * C::ROWS;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -534,7 +609,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
 #pragma unroll
           for (int y = 0; y < NG; ++y) {
             const float z = sum_over_rows(zs[nt][y][hh]);
-            const float up = pow2i(es[y]);
+            const float up = 1.0f / unit[y];  // a power of two
             float v[8];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
@@ -544,7 +619,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
             if (row < nrows) {
               const int ch = 64 * y + 8 * g;
               if (whole) {
-                *reinterpret_cast<uint4*>(a.o + ((size_t)cc.s * a.Hq + hq0 + row) * D + ch) =
+                *reinterpret_cast<uint4*>(a.o + ((size_t)cs * a.Hq + hq0 + row) * D + ch) =
                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                pack_bf16x2(v[6], v[7]));
               } else {
@@ -558,17 +633,20 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
             if (!whole)
               a.part_lse[prow + row] = lse2;
             else if (a.lse != nullptr)
-              a.lse[(size_t)cc.s * a.Hq + hq0 + row] = lse2 * 0.6931471805599453f;
+              a.lse[(size_t)cs * a.Hq + hq0 + row] = lse2 * 0.6931471805599453f;
           }
         }
       if (i + 1 < n) {
-        cc.forward(a, 1);
-        len = kv4_seq_len(a, cc.s);
+        if (++cc == a.Hkv * a.n_hg) {
+          cc = 0;
+          do {  // a row with work follows, since the range goes on
+            ++cs;
+          } while (cs < a.S - 1 && kv4_seq_len(a, cs) == 0);
+        }
+        left = kv4_seq_len(a, cs);
         cut = false;
         begin();
       }
-    } else {
-      ++cc.t;
     }
   }
   cp_async_wait<0>();
@@ -576,19 +654,21 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
 
 // ------------------------------------------------------------------ merge kernel
 
-// One warp per (sequence, query head): joins the partials of a segment that more than one
-// warp's range shares; writes the rows of empty sequences.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) attn_decode_kv4_merge_kernel(const __grid_constant__ DecKv4Args a) {
+// One CTA per (sequence, query head): joins the partials of a segment that more than one warp's
+// range shares; writes the rows of empty sequences.  Its W warps take every W-th partial.  Few
+// rows have many partials each (one per warp of the split kernel that had a part of the row) and
+// get 16 warps; many rows have few each and get 4.  Measured on two rows of 131071 tokens (146
+// partials a head): 21 us with 4 warps, 9 us with 16.
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32) attn_decode_kv4_merge_kernel(const __grid_constant__ DecKv4Args a) {
   using C = DecKv4Cfg<D, NT>;
-  const int wid = (int)((blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5);
-  const int lane = threadIdx.x & 31;
-  if (wid >= a.S * a.Hq) return;
-  const int s = wid / a.Hq, h = wid % a.Hq;
   constexpr int PER = D / 32;
-  const long long p0 = a.tile_prefix[s], p1 = a.tile_prefix[s + 1], per = a.tile_prefix[a.S + 1];
+  __shared__ float sh_m[W], sh_l[W], sh_o[W][D];
+  const int s = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  const long long p0 = a.unit_prefix[s], p1 = a.unit_prefix[s + 1], per = a.unit_prefix[a.S + 1];
   const int nt = (int)(p1 - p0);
-  __nv_bfloat16* dst = a.o + ((size_t)s * a.Hq + h) * D + lane * PER;
   float acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
@@ -598,26 +678,49 @@ __global__ void __launch_bounds__(256) attn_decode_kv4_merge_kernel(const __grid
     const int c = (h / a.group) * a.n_hg + in_kv / C::ROWS;
     const int row = in_kv % C::ROWS;
     const long long f0 = p0 * (a.Hkv * a.n_hg) + (long long)c * nt, f1 = f0 + nt;
-    const long long w0 = f0 / per, w1 = (f1 - 1) / per;
-    if (w0 == w1) return;  // finished by the warp that had all of it
+    const long long w0 = f0 / per;
+    const int np = (int)((f1 - 1) / per - w0) + 1;
+    if (np == 1) return;  // finished by the warp that had all of it
     // the first warp's partial is the one it ended its range with (slot 1), the others' began before them
-    for (long long w = w0; w <= w1; ++w)
-      M = fmaxf(M, a.part_lse[(size_t)(2 * w + (w == w0 ? 1 : 0)) * C::ROWS + row]);
+    auto at = [&](int k) -> size_t { return (size_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row; };
+    for (int k = threadIdx.x; k < np; k += W * 32) M = fmaxf(M, a.part_lse[at(k)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) sh_m[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, sh_m[w]);
     const float u = M == -INFINITY ? 0.f : M;
-    for (long long w = w0; w <= w1; ++w) {
-      const size_t pi = (size_t)(2 * w + (w == w0 ? 1 : 0)) * C::ROWS + row;
-      const float k = ex2(a.part_lse[pi] - u);
-      L += k;
+#pragma unroll 4
+    for (int k = warp; k < np; k += W) {
+      const size_t pi = at(k);
+      const float e = ex2(a.part_lse[pi] - u);
+      L += e;
       const float* po = a.part_o + pi * D + lane * PER;
 #pragma unroll
       for (int i = 0; i < PER; i += 2) {
         const float2 v = *reinterpret_cast<const float2*>(po + i);
-        acc[i] = fmaf(k, v.x, acc[i]);
-        acc[i + 1] = fmaf(k, v.y, acc[i + 1]);
+        acc[i] = fmaf(e, v.x, acc[i]);
+        acc[i + 1] = fmaf(e, v.y, acc[i + 1]);
       }
     }
+    if (lane == 0) sh_l[warp] = L;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sh_o[warp][lane * PER + i] = acc[i];
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      L += sh_l[w];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += sh_o[w][lane * PER + i];
+    }
   }
+  if (warp != 0) return;
   const float inv = L != 0.f ? 1.f / L : 0.f;
+  __nv_bfloat16* dst = a.o + ((size_t)s * a.Hq + h) * D + lane * PER;
 #pragma unroll
   for (int i = 0; i < PER; i += 2)
     *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);

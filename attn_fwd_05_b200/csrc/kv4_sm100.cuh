@@ -95,6 +95,11 @@ __device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8])
     xv[2 * i] = bf16lo_to_f32(w[i]);
     xv[2 * i + 1] = bf16hi_to_f32(w[i]);
   }
+  if (span == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+    return (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
+  }
   bool redo = s < 7.7e-34f;  // 2^-110: rcp(s) may overflow
   if (!redo) {
     float inv;
@@ -112,7 +117,7 @@ __device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8])
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double q = ((double)xv[i] - (double)lo) / (double)s;
-      r[i] = q >= 0.0 ? (float)fmin(rint(q), 15.0) : 0.0f;  // 0 / 0 (a constant group): code 0
+      r[i] = q >= 0.0 ? (float)fmin(rint(q), 15.0) : 0.0f;  // 0 / 0 (the scale underflowed): code 0
     }
   }
   return (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
