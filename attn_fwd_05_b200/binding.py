@@ -306,23 +306,36 @@ def attn_decode_paged_noalloc(q, k_pool, v_pool, block_table, seq_lens, page_siz
     _check(st, "attn_decode_paged_noalloc")
 
 
-def _same_device(*tensors) -> None:
-    """The tensors of a call lie on the current CUDA device, where its kernels will run."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{cur}")
+def _current_device() -> int:
+    """Number of the current CUDA device; one that no tensor has where there is no device."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
 
 
-def _kv4_pool(kv_pool, block_table, seq_lens, page_size: int, d: int) -> tuple:
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, dev: int) -> int:
+    """Address of a dense tensor on device `dev` (the current one, where the call's kernels run)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.dim() == ndim:
+        return t.data_ptr()
+    _dev(t, name, dtype, ndim)  # says what is wrong, unless it is the device
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _scratch(workspace: torch.Tensor, dev: int) -> tuple[int, int]:
+    """Address and bytes of a workspace (any type and shape)."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    return _ptr(workspace, "workspace", workspace.dtype, workspace.dim(), dev), workspace.nbytes
+
+
+def _kv4_pool(kv_pool, block_table, seq_lens, page_size: int, d: int, dev: int) -> tuple:
     """Checks a 4-bit pool and its table: ((pool, table, lens) addresses, S, Hkv, num_pages, max_pages)."""
-    ptrs = (_dev(kv_pool, "kv_pool", torch.uint8), _dev(block_table, "block_table", torch.int32, 2),
-            _dev(seq_lens, "seq_lens", torch.int32, 1))
+    ptrs = (_ptr(kv_pool, "kv_pool", torch.uint8, 3, dev), _ptr(block_table, "block_table", torch.int32, 2, dev),
+            _ptr(seq_lens, "seq_lens", torch.int32, 1, dev))
     S, max_pages = block_table.shape
     if seq_lens.shape[0] != S:
         raise ValueError("seq_lens must be [num_seqs] with block_table's num_seqs")
-    if kv_pool.dim() != 3:
-        raise ValueError("kv_pool must be [num_pages, Hkv, page_size * d * 9 / 8]")
     num_pages, Hkv, head_bytes = kv_pool.shape
     if head_bytes * 8 != page_size * d * 9:
         raise ValueError(f"kv_pool must be [num_pages, Hkv, page_size * d * 9 / 8] = [.., .., {page_size * d * 9 // 8}]")
@@ -334,19 +347,21 @@ def attn_kv4_page_bytes(Hkv: int, page_size: int, d: int) -> int:
     return int(load_library().attn_kv4_page_bytes(Hkv, page_size, d))
 
 
-def _token_rows(t, name: str, T: int, Hkv: int, d: int) -> tuple[int, int]:
+def _token_rows(t, name: str, shape, dev: int) -> tuple[int, int]:
     """Address and token stride of a bf16 [T, Hkv, d] tensor whose tokens are dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.shape != (T, Hkv, d):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on a CUDA device, the current one")
+    if t.shape != shape:
         raise ValueError(f"{name} must be [num_new, Hkv, d]")
-    if (d > 1 and t.stride(2) != 1) or (Hkv > 1 and t.stride(1) != d):
+    T, Hkv, d = shape
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (Hkv > 1 and sh != d):
         raise ValueError(f"the heads and channels of a token of {name} must be dense")
-    return t.data_ptr(), t.stride(0) if T > 1 else Hkv * d
+    return t.data_ptr(), st if T > 1 else Hkv * d
 
 
 def attn_kv4_append(k: torch.Tensor, v: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
@@ -355,47 +370,46 @@ def attn_kv4_append(k: torch.Tensor, v: torch.Tensor, kv_pool: torch.Tensor, blo
     """Quantizes bf16 k and v [num_new, Hkv, d] (any token stride) into the 4-bit pool: rows
     cu_new[s]..cu_new[s+1]-1 are the last tokens of sequence s, whose length seq_lens[s] includes them.
     k_out and v_out (bf16 [num_new, Hkv, d]) receive the values the cache then stands for."""
-    lib = load_library()
+    lib = _LIB or load_library()
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise TypeError("k must be a torch.Tensor [num_new, Hkv, d]")
-    T, Hkv, d = k.shape
-    kp, ks = _token_rows(k, "k", T, Hkv, d)
-    vp, vs = _token_rows(v, "v", T, Hkv, d)
-    (pool, table, lens), S, pool_heads, num_pages, max_pages = _kv4_pool(kv_pool, block_table, seq_lens, page_size, d)
+    dev = _current_device()
+    shape = k.shape
+    T, Hkv, d = shape
+    kp, ks = _token_rows(k, "k", shape, dev)
+    vp, vs = _token_rows(v, "v", shape, dev)
+    (pool, table, lens), S, pool_heads, num_pages, max_pages = _kv4_pool(kv_pool, block_table, seq_lens, page_size, d,
+                                                                         dev)
     if pool_heads != Hkv:
         raise ValueError("k and kv_pool must have the same number of KV heads")
-    cu = _dev(cu_new, "cu_new", torch.int32, 1)
+    cu = _ptr(cu_new, "cu_new", torch.int32, 1, dev)
     if cu_new.shape[0] != S + 1:
         raise ValueError("cu_new must be [num_seqs + 1]")
-    ko, vo = None, None
-    if k_out is not None:
-        ko = _dev(k_out, "k_out", torch.bfloat16)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must be [num_new, Hkv, d]")
-    if v_out is not None:
-        vo = _dev(v_out, "v_out", torch.bfloat16)
-        if v_out.shape != k.shape:
-            raise ValueError("v_out must be [num_new, Hkv, d]")
-    _same_device(k, v, kv_pool, block_table, seq_lens, cu_new, k_out, v_out)
+    ko = None if k_out is None else _ptr(k_out, "k_out", torch.bfloat16, 3, dev)
+    vo = None if v_out is None else _ptr(v_out, "v_out", torch.bfloat16, 3, dev)
+    if (ko is not None and k_out.shape != shape) or (vo is not None and v_out.shape != shape):
+        raise ValueError("k_out and v_out must be [num_new, Hkv, d]")
     st = lib.attn_kv4_append(kp, vp, ks, vs, pool, table, lens, cu, page_size, ko, vo, S, T, Hkv, d, num_pages,
                              max_pages, _stream(stream))
-    _check(st, "attn_kv4_append")
+    if st:
+        _check(st, "attn_kv4_append")
 
 
 def attn_kv4_gather(kv_pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int,
                     k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Reads the first min(seq_lens[s], N) cached tokens of every sequence into bf16 k and v
     [num_seqs, Hkv, N, d] (attn_fwd's layout); rows past a sequence's end keep what they hold."""
-    lib = load_library()
-    kp, vp = _dev(k, "k", torch.bfloat16, 4), _dev(v, "v", torch.bfloat16, 4)
-    d, N = k.shape[3], k.shape[2]
-    (pool, table, lens), S, Hkv, num_pages, max_pages = _kv4_pool(kv_pool, block_table, seq_lens, page_size, d)
-    if k.shape != (S, Hkv, N, d) or v.shape != k.shape:
+    lib = _LIB or load_library()
+    dev = _current_device()
+    kp, vp = _ptr(k, "k", torch.bfloat16, 4, dev), _ptr(v, "v", torch.bfloat16, 4, dev)
+    rows, heads, N, d = k.shape
+    (pool, table, lens), S, Hkv, num_pages, max_pages = _kv4_pool(kv_pool, block_table, seq_lens, page_size, d, dev)
+    if rows != S or heads != Hkv or v.shape != k.shape:
         raise ValueError("k and v must be [num_seqs, Hkv, N, d]")
-    _same_device(kv_pool, block_table, seq_lens, k, v)
     st = lib.attn_kv4_gather(pool, table, lens, page_size, kp, vp, S, Hkv, N, d, num_pages, max_pages,
                              _stream(stream))
-    _check(st, "attn_kv4_gather")
+    if st:
+        _check(st, "attn_kv4_gather")
 
 
 def attn_decode_paged_kv4_workspace_size(num_seqs: int, Hq: int, Hkv: int, d: int) -> int:
@@ -406,37 +420,41 @@ def attn_decode_paged_kv4(q: torch.Tensor, kv_pool: torch.Tensor, block_table: t
                           page_size: int, o: torch.Tensor, lse: torch.Tensor | None, scale: float,
                           workspace: torch.Tensor, stream=None) -> None:
     """One decode step over a 4-bit paged cache: q and o bf16 [num_seqs, Hq, d], lse fp32 [num_seqs, Hq] or None."""
-    lib = load_library()
-    qp, op = _dev(q, "q", torch.bfloat16, 3), _dev(o, "o", torch.bfloat16, 3)
-    S, Hq, d = q.shape
-    (pool, table, lens), rows, Hkv, num_pages, max_pages = _kv4_pool(kv_pool, block_table, seq_lens, page_size, d)
+    lib = _LIB or load_library()
+    dev = _current_device()
+    qp, op = _ptr(q, "q", torch.bfloat16, 3, dev), _ptr(o, "o", torch.bfloat16, 3, dev)
+    shape = q.shape
+    S, Hq, d = shape
+    (pool, table, lens), rows, Hkv, num_pages, max_pages = _kv4_pool(kv_pool, block_table, seq_lens, page_size, d, dev)
     if rows != S:
         raise ValueError("block_table must be [num_seqs, max_pages_per_seq] with q's num_seqs")
-    if o.shape != q.shape:
+    if o.shape != shape:
         raise ValueError("o must be [num_seqs, Hq, d]")
     lp = None
     if lse is not None:
-        lp = _dev(lse, "lse", torch.float32, 2)
+        lp = _ptr(lse, "lse", torch.float32, 2, dev)
         if lse.shape != (S, Hq):
             raise ValueError("lse must be [num_seqs, Hq]")
-    ws = _dev(workspace, "workspace", workspace.dtype)
-    _same_device(q, kv_pool, block_table, seq_lens, o, lse, workspace)
+    ws, nbytes = _scratch(workspace, dev)
     st = lib.attn_decode_paged_kv4(qp, pool, table, lens, page_size, op, lp, S, Hq, Hkv, d, num_pages, max_pages,
-                                   scale, ws, workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "attn_decode_paged_kv4")
+                                   scale, ws, nbytes, _stream(stream))
+    if st:
+        _check(st, "attn_decode_paged_kv4")
 
 
-def _page_pools(pools) -> tuple:
+def _page_pools(pools, dev: int) -> tuple:
     """Checks pools that share a table: (pointer array, count, bytes per page, num_pages)."""
     if len(pools) == 0:
         raise ValueError("pools must hold at least one tensor [num_pages, ...]")
-    num_pages = pools[0].shape[0]
-    nbytes = pools[0].numel() * pools[0].element_size()
-    for p in pools:
-        _dev(p, "a pool", p.dtype)
-        if p.dim() < 2 or p.shape[0] != num_pages or p.numel() * p.element_size() != nbytes:
+    first = pools[0]
+    if not isinstance(first, torch.Tensor) or first.dim() < 2:
+        raise TypeError("a pool must be a torch.Tensor [num_pages, ...]")
+    num_pages, nbytes = first.shape[0], first.nbytes
+    ptrs = (ctypes.c_void_p * len(pools))()
+    for i, p in enumerate(pools):
+        ptrs[i] = _ptr(p, "a pool", p.dtype, p.dim(), dev)
+        if p.dim() < 2 or p.shape[0] != num_pages or p.nbytes != nbytes:
             raise ValueError("pools must be [num_pages, ...] with the same number and size of pages")
-    ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
     return ptrs, len(pools), nbytes // num_pages if num_pages else 0, num_pages
 
 
@@ -451,11 +469,12 @@ def attn_pages_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: 
     """Builds new_table and new_lens: row i continues row parents[i] of the old table (-1: empty) with
     add_tokens[i] tokens more (or fewer).  Full pages are shared, a part-filled last page is copied for
     all but one of the rows that continue it (in every pool), new pages come from the free ones."""
-    lib = load_library()
-    args = (_dev(block_table, "block_table", torch.int32, 2), _dev(seq_lens, "seq_lens", torch.int32, 1),
-            _dev(parents, "parents", torch.int32, 1),
-            None if add_tokens is None else _dev(add_tokens, "add_tokens", torch.int32, 1),
-            _dev(new_table, "new_table", torch.int32, 2), _dev(new_lens, "new_lens", torch.int32, 1))
+    lib = _LIB or load_library()
+    dev, i32 = _current_device(), torch.int32
+    args = (_ptr(block_table, "block_table", i32, 2, dev), _ptr(seq_lens, "seq_lens", i32, 1, dev),
+            _ptr(parents, "parents", i32, 1, dev),
+            None if add_tokens is None else _ptr(add_tokens, "add_tokens", i32, 1, dev),
+            _ptr(new_table, "new_table", i32, 2, dev), _ptr(new_lens, "new_lens", i32, 1, dev))
     S, cols = block_table.shape
     rows, new_cols = new_table.shape
     if seq_lens.shape[0] != S or parents.shape[0] != rows or new_lens.shape[0] != rows or \
@@ -463,13 +482,13 @@ def attn_pages_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: 
         raise ValueError("seq_lens must be [num_seqs]; parents, add_tokens and new_lens [new_rows]")
     if n_free is not None and n_free.numel() != 1:
         raise ValueError("n_free must hold one number")
-    ptrs, n, page_bytes, num_pages = _page_pools(pools)
-    ws = _dev(workspace, "workspace", workspace.dtype)
-    _same_device(block_table, seq_lens, parents, add_tokens, new_table, new_lens, n_free, workspace, *pools)
+    ptrs, n, page_bytes, num_pages = _page_pools(pools, dev)
+    ws, nbytes = _scratch(workspace, dev)
     st = lib.attn_pages_fork(*args, page_size, ptrs, n, page_bytes, S, cols, rows, new_cols, num_pages,
-                             None if n_free is None else _dev(n_free, "n_free", torch.int32), ws,
-                             workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "attn_pages_fork")
+                             None if n_free is None else _ptr(n_free, "n_free", i32, n_free.dim(), dev), ws, nbytes,
+                             _stream(stream))
+    if st:
+        _check(st, "attn_pages_fork")
 
 
 def attn_pages_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, new_table: torch.Tensor,
@@ -477,23 +496,24 @@ def attn_pages_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, new_ta
                        n_live: torch.Tensor | None = None, stream=None) -> None:
     """Renumbers the n pages in use to 0..n-1, moving their contents in every pool: new_table (may be
     block_table) and page_map int32 [num_pages] (new number of each page, -1: free)."""
-    lib = load_library()
-    args = (_dev(block_table, "block_table", torch.int32, 2), _dev(seq_lens, "seq_lens", torch.int32, 1),
-            _dev(new_table, "new_table", torch.int32, 2), _dev(page_map, "page_map", torch.int32, 1))
+    lib = _LIB or load_library()
+    dev, i32 = _current_device(), torch.int32
+    args = (_ptr(block_table, "block_table", i32, 2, dev), _ptr(seq_lens, "seq_lens", i32, 1, dev),
+            _ptr(new_table, "new_table", i32, 2, dev), _ptr(page_map, "page_map", i32, 1, dev))
     S, cols = block_table.shape
     if seq_lens.shape[0] != S or new_table.shape != block_table.shape:
         raise ValueError("seq_lens must be [num_seqs] and new_table [num_seqs, max_pages_per_seq]")
     if n_live is not None and n_live.numel() != 1:
         raise ValueError("n_live must hold one number")
-    ptrs, n, page_bytes, num_pages = _page_pools(pools)
+    ptrs, n, page_bytes, num_pages = _page_pools(pools, dev)
     if page_map.shape[0] != num_pages:
         raise ValueError("page_map must be [num_pages]")
-    ws = _dev(workspace, "workspace", workspace.dtype)
-    _same_device(block_table, seq_lens, new_table, page_map, n_live, workspace, *pools)
+    ws, nbytes = _scratch(workspace, dev)
     st = lib.attn_pages_compact(*args, page_size, ptrs, n, page_bytes, S, cols, num_pages,
-                                None if n_live is None else _dev(n_live, "n_live", torch.int32), ws,
-                                workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "attn_pages_compact")
+                                None if n_live is None else _ptr(n_live, "n_live", i32, n_live.dim(), dev), ws, nbytes,
+                                _stream(stream))
+    if st:
+        _check(st, "attn_pages_compact")
 
 
 def attn_get_device_status(stream=None) -> int:

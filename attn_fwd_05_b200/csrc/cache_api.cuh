@@ -33,7 +33,7 @@ attn_status launch_append(const attn::Kv4AppendArgs& a, unsigned grid, cudaStrea
 
 template <int NG>
 attn_status launch_gather(const attn::Kv4GatherArgs& a, unsigned grid, cudaStream_t st) {
-  attn::attn_kv4_gather_kernel<NG><<<grid, 256, 0, st>>>(a);
+  attn::attn_kv4_gather_kernel<NG><<<grid, attn::Kv4GatherCfg<NG>::WARPS * 32, 0, st>>>(a);
   return launch_status();
 }
 
@@ -176,8 +176,10 @@ attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int6
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.max_pages = max_pages_per_seq;
-  const long long units = ((long long)(num_new >> 2) + 2ll * num_seqs) * Hkv;
-  const long long grid = (units + 7) / 8;
+  // as many heads a warp as leave some 48 warps to every SM
+  const long long quads = (long long)(num_new >> 2) + 2ll * num_seqs;
+  a.heads = (int)std::max(1ll, std::min<long long>(Hkv, quads * Hkv / (48ll * sm_count())));
+  const long long grid = (quads * ((Hkv + a.heads - 1) / a.heads) + 7) / 8;
   if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d) {
@@ -213,8 +215,10 @@ attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, con
   // N may be larger than any row: records past a row's capacity have no work
   const long long nrec = ((long long)N + 15) / 16;
   const long long units = nrec * num_seqs;
-  if (units > 0x7fffffffLL * 8 / Hkv) return ATTN_ERR_INVALID_ARG;
-  const unsigned grid = (unsigned)((units * Hkv + 7) / 8);
+  if (units > 0x7fffffffLL * 4 / Hkv) return ATTN_ERR_INVALID_ARG;
+  a.heads = (int)std::max(1ll, std::min<long long>(Hkv, units * Hkv / (48ll * sm_count())));
+  const int warps = d == 256 ? 4 : 8;
+  const unsigned grid = (unsigned)((units * ((Hkv + a.heads - 1) / a.heads) + warps - 1) / warps);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d) {
     case 64: return launch_gather<1>(a, grid, st);

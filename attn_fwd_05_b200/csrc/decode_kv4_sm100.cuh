@@ -86,15 +86,6 @@ __device__ __forceinline__ void mma_16816_f16_first(float (&c)[4], uint32_t a0, 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// a b + c with bf16 a and b (16-bit halves of a parameter word, say) and fp32 c: one FMA, where
-// widening a half first would cost an instruction of the half-rate integer pipe.
-__device__ __forceinline__ float fma_bf16(uint32_t a, uint32_t b, float c) {
-  float d;
-  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"((uint16_t)a), "h"((uint16_t)b), "f"(c));
-  return d;
-}
-constexpr uint32_t kBf16One = 0x3f80u, kBf16Eight = 0x4100u;
-
 // Programmatic dependent launch: the dependent grid may be set up from here on; it waits for this
 // grid's end (and its writes) in pdl_wait.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -105,15 +96,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -337,13 +319,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
       for (int x = 0; x < 2; ++x) {
         const int rec = x == 0 ? r0 : r1;
         if (rec >= 0) {
-          const uint8_t* src = a.pool + (size_t)rec * C::REC + lane * 16;
-          const uint32_t dst = in + x * C::REC + lane * 16;
-#pragma unroll
-          for (int i = 0; i < C::REC / 512; ++i) cp_async16(dst + i * 512, src + i * 512);
-          if constexpr (C::REC % 512 != 0) {
-            if (lane < (C::REC % 512) / 16) cp_async16(dst + C::REC / 512 * 512, src + C::REC / 512 * 512);
-          }
+          kv4_fetch_record<C::REC>(in + x * C::REC, a.pool + (size_t)rec * C::REC, lane);
         }
       }
     }
@@ -486,9 +462,18 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
             for (int y = 0; y < NG; ++y) sts_word(out + tile * C::REC + 1088 * NG + ((2 * g + r) * NG + y) * 4, 0u);
           }
       __syncwarp();
+#pragma unroll
+      for (int y = 0; y < NG; ++y) smax[y] = 0u;  // without the masked slots: the result must not depend on them
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        uint32_t vp[2 * NG];
+        lds_params<NG>(out + tile * C::REC + 1088 * NG + g * 8 * NG, vp);
+#pragma unroll
+        for (int y = 0; y < NG; ++y) smax[y] = max_u16x2(smax[y], max_u16x2(vp[y], vp[NG + y]));
+      }
     }
     // ---- references: raised when a score passes m by 8, or a V scale 2^es by 2^6 (scales are not
-    // negative, so their bits order like the values; a masked slot may only cause a needless look)
+    // negative, so their bits order like the values)
     bool raise = false;
     float top[NT][2];
 #pragma unroll

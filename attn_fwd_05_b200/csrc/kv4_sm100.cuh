@@ -53,16 +53,44 @@ struct Kv4AppendArgs {
   __nv_bfloat16* v_out;
   long long k_stride, v_stride;
   int S, T, Hkv, page_size, num_pages, max_pages;
+  int heads;  // KV heads a warp takes in turn
 };
+
+// a b + c with bf16 a and b (16-bit halves of a word, say) and fp32 c: one FMA, where widening
+// a half first would cost an instruction of the half-rate integer pipe.
+__device__ __forceinline__ float fma_bf16(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"((uint16_t)a), "h"((uint16_t)b), "f"(c));
+  return d;
+}
+constexpr uint32_t kBf16One = 0x3f80u, kBf16Eight = 0x4100u;
+
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+// Bits of |x| less one, for both bf16 halves of a word (0 becomes 0xffff).
+__device__ __forceinline__ uint32_t magnitude_less_one(uint32_t w) {
+  uint32_t c;
+  asm("add.u16x2 %0, %1, %2;" : "=r"(c) : "r"(w & 0x7fff7fffu), "r"(0xffffffffu));
+  return c;
+}
 
 // One lane's 8 channels of a group whose 64 channels lie in 8 neighbouring lanes: the group's
 // scale and minimum (packed s | m << 16) and the codes as floats in r[0..7].
 //
-// c = nearest integer to (x - m) / s, ties to even, of the exact quotient.  The fast path forms
-// (x - m) * rcp(s): the subtraction is exact or off by 2^-24, the product by 2^-22 relative,
-// so for quotients up to 15.1 the value is within 2^-17 of the exact one; a value that close to
-// a border between two codes (k + 1/2) is redone in 64 bits, where the quotient of these
-// 8-bit significands is never rounded onto or across a border.
+// c = nearest integer to (x - m) / s, ties to even, of the exact quotient.  Values of few
+// significant bits meet a border k + 1/2 between two codes often, so borders have to be exact on
+// the fast path: u = x - m, a first quotient u * rcp(s), and one correction by its remainder
+// give the quotient within half an ulp (2^-21 up to 16), and exactly where it is representable, as
+// a border is.  That suffices while no |x| or |m| but 0 is below 2^-12 s: x and m are then
+// multiples of 2^-20 s (8 significant bits), u needs fewer than 24 bits and is exact, and a
+// quotient that is no border is at least 2^-20 away from one.  Other groups are redone in 64 bits.
+//
+// The scale's division by 15 is a product with 1/15 and one correction by its remainder, which
+// gives the correctly rounded quotient for every 24-bit significand (checked exhaustively).
 __device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   __nv_bfloat162 h[4];
@@ -80,43 +108,50 @@ __device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8])
     e = __hmin2_nan(e, *reinterpret_cast<__nv_bfloat162*>(&u));
   }
   const float lo = __low2float(e) + 0.0f;  // a zero minimum is stored as +0
-  const float hi = 0.0f - __high2float(e);
-  const float span = hi - lo;
-  if (!(span <= 3.4028234663852886e38f)) {  // infinite or NaN values, or a range past fp32: the group is NaN
+  const float span = -__high2float(e) - lo + 0.0f;
+  float q15 = span * (1.0f / 15.0f);
+  q15 = fmaf(fmaf(-15.0f, q15, span), 1.0f / 15.0f, q15);
+  // 2^-100 <= span: neither the remainder above nor rcp(s) below leaves the normal numbers
+  const bool plain = span >= 7.888609e-31f && span <= 3.4028234663852886e38f;
+  if (!plain) {
+    if (!(span <= 3.4028234663852886e38f)) {  // infinite or NaN values, or a range past fp32: the group is NaN
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-    return 0x7fc07fc0u;
+      for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+      return 0x7fc07fc0u;
+    }
+    q15 = __fdiv_rn(span, 15.0f);
   }
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(span, 15.0f));
+  const __nv_bfloat16 sb = __float2bfloat16_rn(q15);
   const float s = __bfloat162float(sb);
-  float xv[8];
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    xv[2 * i] = bf16lo_to_f32(w[i]);
-    xv[2 * i + 1] = bf16hi_to_f32(w[i]);
+    constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to the nearest integer, ties to even
+    const float u0 = fma_bf16(w[i], kBf16One, -lo), u1 = fma_bf16(w[i] >> 16, kBf16One, -lo);
+    float q0 = u0, q1 = u1, e0, e1;
+    mul2(q0, q1, inv, inv);
+    fma2(e0, e1, q0, q1, -s, -s, u0, u1);
+    fma2(q0, q1, e0, e1, inv, inv, q0, q1);
+    add2(q0, q1, kRound, kRound);
+    add2(q0, q1, -kRound, -kRound);
+    r[2 * i] = q0;
+    r[2 * i + 1] = q1;
   }
-  if (span == 0.0f) {
+  // magnitudes order like their bits; a zero becomes the largest
+  const uint32_t least = min_u16x2(min_u16x2(magnitude_less_one(w[0]), magnitude_less_one(w[1])),
+                                   min_u16x2(magnitude_less_one(w[2]), magnitude_less_one(w[3])));
+  const uint32_t small = __float_as_uint(s * 0.000244140625f) >> 16;  // 2^-12 s
+  const bool fine = plain && min(least & 0xffffu, least >> 16) >= small &&
+                    ((__float_as_uint(lo) >> 16) & 0x7fffu) - 1u >= small;
+  if (span == 0.0f) {  // a constant group, or a token that is not there
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-    return (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
-  }
-  bool redo = s < 7.7e-34f;  // 2^-110: rcp(s) may overflow
-  if (!redo) {
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    float far = 0.0f;
+  } else if (!fine) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float u = (xv[i] - lo) * inv;
-      r[i] = (u + 12582912.0f) - 12582912.0f;  // 1.5 * 2^23: round to the nearest integer
-      far = fmaxf(far, fabsf(u - r[i]));
-    }
-    redo = far > 0.5f - 1.52587890625e-5f;  // 2^-16
-  }
-  if (redo) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double q = ((double)xv[i] - (double)lo) / (double)s;
+      const float xi = i % 2 == 0 ? bf16lo_to_f32(w[i / 2]) : bf16hi_to_f32(w[i / 2]);
+      const double q = ((double)xi - (double)lo) / (double)s;
       r[i] = q >= 0.0 ? (float)fmin(rint(q), 15.0) : 0.0f;  // 0 / 0 (the scale underflowed): code 0
     }
   }
@@ -126,8 +161,24 @@ __device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8])
 // Values s c + m of 8 codes, rounded to bf16.
 __device__ __forceinline__ uint4 kv4_values8(const float (&r)[8], uint32_t sm) {
   const float s = bf16lo_to_f32(sm), m = bf16hi_to_f32(sm);
-  return make_uint4(pack_bf16x2(fmaf(s, r[0], m), fmaf(s, r[1], m)), pack_bf16x2(fmaf(s, r[2], m), fmaf(s, r[3], m)),
-                    pack_bf16x2(fmaf(s, r[4], m), fmaf(s, r[5], m)), pack_bf16x2(fmaf(s, r[6], m), fmaf(s, r[7], m)));
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fma2(v[2 * i], v[2 * i + 1], r[2 * i], r[2 * i + 1], s, s, m, m);
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// The same from a word of codes: pairs (nibble i of the low half, nibble i of the high half), i =
+// 0..3, as bf16 integers.  A code masked into the mantissa of 128 is 128 + c; the subtraction is exact.
+__device__ __forceinline__ void kv4_code_values(uint32_t w, uint32_t sm, float (&lo)[4], float (&hi)[4]) {
+  const float m = bf16hi_to_f32(sm);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t c = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(c) : "r"(c), "r"(0x3f803f80u), "r"(0xc300c300u));
+    lo[i] = fma_bf16(sm, c, m);
+    hi[i] = fma_bf16(sm, c >> 16, m);
+  }
 }
 
 // Largest s in [0, S) with (cu[s] >> 2) + 2 s <= q: sequence s owns the quads from there on.
@@ -147,16 +198,21 @@ __device__ __forceinline__ int kv4_find_seq(const int32_t* cu, int S, long long 
   return lo;
 }
 
-// One warp per (aligned quad of positions, KV head): lane = 8 (token of the quad) + (8-channel
-// chunk).  The reads are bf16 rows of 128 bytes a group; the quad's K codes and V codes are
-// one 128-byte line a group each.
+// One warp per aligned quad of positions and `heads` KV heads: lane = 8 (token of the quad) +
+// (8-channel chunk).  The reads are bf16 rows of 128 bytes a group; the quad's K codes and V codes
+// are one 128-byte line a group each.  A call is bound by HBM (2 d bytes read and 9 d / 16
+// written per token, head and tensor) once every SM has enough loads in flight: a warp therefore
+// takes several heads where there are warps to spare, since its chain of dependent loads (sequence,
+// position, page) then serves all of them, and fetches the next head's rows while it works
+// on one.  108K tokens, 8 heads, d = 128, with the values written back: @@.
 template <int NG>
 __global__ void __launch_bounds__(256) attn_kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
   constexpr int D = NG * kKv4Group;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const long long q = unit / a.Hkv;
-  const int h = (int)(unit % a.Hkv);
+  const int parts = (a.Hkv + a.heads - 1) / a.heads;
+  const long long q = unit / parts;
+  const int h0 = (int)(unit % parts) * a.heads, h1 = min(a.Hkv, h0 + a.heads);
   if (q >= (a.T >> 2) + 2ll * a.S) return;
   const int s = kv4_find_seq(a.cu_new, a.S, q, lane);
   const int c0 = __ldg(&a.cu_new[s]), c1 = __ldg(&a.cu_new[s + 1]);
@@ -175,59 +231,81 @@ __global__ void __launch_bounds__(256) attn_kv4_append_kernel(const __grid_const
   const bool live = pos >= start && pos < len;
   const int page = __ldg(&a.block_table[(size_t)s * a.max_pages + (4 * quad) / a.page_size]);
   const int tok = c0 + (pos - start);
-  const size_t head = (size_t)h * D + 8 * j;
-  uint4 kx[NG], vx[NG];
+  const __nv_bfloat16* kp = a.k + (size_t)tok * a.k_stride + 8 * j;
+  const __nv_bfloat16* vp = a.v + (size_t)tok * a.v_stride + 8 * j;
+  uint4 kn[NG], vn[NG];
+  auto fetch = [&](int h) {
 #pragma unroll
-  for (int y = 0; y < NG; ++y) {
-    kx[y] = vx[y] = make_uint4(0, 0, 0, 0);
-    if (live) {
-      kx[y] = __ldg(reinterpret_cast<const uint4*>(a.k + (size_t)tok * a.k_stride + head + 64 * y));
-      vx[y] = __ldg(reinterpret_cast<const uint4*>(a.v + (size_t)tok * a.v_stride + head + 64 * y));
+    for (int y = 0; y < NG; ++y) {
+      kn[y] = vn[y] = make_uint4(0, 0, 0, 0);
+      if (live) {
+        kn[y] = __ldg(reinterpret_cast<const uint4*>(kp + (size_t)h * D + 64 * y));
+        vn[y] = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)h * D + 64 * y));
+      }
     }
-  }
+  };
+  fetch(h0);
   if (page < 0 || page >= a.num_pages) {
     latch_status(ATTN_ERR_BAD_PAGE);
     return;
   }
   const int blocks = a.page_size / kKv4Tok;
   const int in_page = (int)(4 * quad) % a.page_size;
-  uint8_t* rec = a.pool + (((size_t)page * a.Hkv + h) * blocks + in_page / kKv4Tok) * kv4_record_bytes(D);
+  uint8_t* rec = a.pool + (((size_t)page * a.Hkv + h0) * blocks + in_page / kKv4Tok) * kv4_record_bytes(D);
   const int ta = (in_page >> 2) & 3, b0 = i & 1, b1 = i >> 1;
   const bool pair_live = __shfl_xor_sync(0xffffffffu, live ? 1 : 0, 8) && live;
-  uint32_t par = 0;  // the parameter word this lane stores: lanes 0.. of K's groups, lanes 4.. of V's
+  size_t out = ((size_t)tok * a.Hkv + h0) * D + 8 * j;
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    uint4 kx[NG], vx[NG];
 #pragma unroll
-  for (int y = 0; y < NG; ++y) {
-    float r[8];
-    uint32_t sm = kv4_quantize8(kx[y], r);
-    if (j == y) par = sm;
-    // even channels into the low half, odd ones into the high half; both sums are below 2^16
-    const float ev = r[0] + 16.0f * r[2] + 256.0f * r[4] + 4096.0f * r[6];
-    const float od = r[1] + 16.0f * r[3] + 256.0f * r[5] + 4096.0f * r[7];
-    const uint32_t kw = (uint32_t)ev | ((uint32_t)od << 16);
-    if (live) {
-      *reinterpret_cast<uint32_t*>(rec + kv4_k_code_off(y, ta, b0, b1, j)) = kw;
-      if (a.k_out != nullptr)
-        *reinterpret_cast<uint4*>(a.k_out + (size_t)tok * a.Hkv * D + head + 64 * y) = kv4_values8(r, sm);
+    for (int y = 0; y < NG; ++y) {
+      kx[y] = kn[y];
+      vx[y] = vn[y];
     }
-    sm = kv4_quantize8(vx[y], r);
-    if (j == 4 + y) par = sm;
-    const float c03 = r[0] + 16.0f * r[1] + 256.0f * r[2] + 4096.0f * r[3];
-    const float c47 = r[4] + 16.0f * r[5] + 256.0f * r[6] + 4096.0f * r[7];
-    const uint32_t vw = (uint32_t)c03 | ((uint32_t)c47 << 16);
-    // a word holds both tokens of a pair: the even token's lane writes channels 0-3, the odd one's 4-7
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, 8);
-    uint8_t* unit_v = rec + kv4_v_unit_off<NG>(y, ta, j) + 8 * b1;
-    if (pair_live) {
-      *reinterpret_cast<uint32_t*>(unit_v + 4 * b0) = b0 == 0 ? __byte_perm(vw, other, 0x5410) : __byte_perm(other, vw, 0x7632);
-    } else if (live) {
-      *reinterpret_cast<uint16_t*>(unit_v + 2 * b0) = (uint16_t)(vw & 0xffffu);
-      *reinterpret_cast<uint16_t*>(unit_v + 4 + 2 * b0) = (uint16_t)(vw >> 16);
+    if (h + 1 < h1) fetch(h + 1);
+    uint32_t par = 0;  // the parameter word this lane stores: lanes 0.. of K's groups, lanes 4.. of V's
+#pragma unroll
+    for (int y = 0; y < NG; ++y) {
+      float r[8];
+      uint32_t sm = kv4_quantize8(kx[y], r);
+      if (j == y) par = sm;
+      // even channels into the low half, odd ones into the high half; both sums are below 2^16,
+      // and adding 2^23 leaves them in the low bits
+      float ev = r[6], od = r[7];
+      fma2(ev, od, ev, od, 16.0f, 16.0f, r[4], r[5]);
+      fma2(ev, od, ev, od, 16.0f, 16.0f, r[2], r[3]);
+      fma2(ev, od, ev, od, 16.0f, 16.0f, r[0], r[1]);
+      add2(ev, od, 8388608.0f, 8388608.0f);
+      const uint32_t kw = __byte_perm(__float_as_uint(ev), __float_as_uint(od), 0x5410);
+      if (live) {
+        *reinterpret_cast<uint32_t*>(rec + kv4_k_code_off(y, ta, b0, b1, j)) = kw;
+        if (a.k_out != nullptr) *reinterpret_cast<uint4*>(a.k_out + out + 64 * y) = kv4_values8(r, sm);
+      }
+      sm = kv4_quantize8(vx[y], r);
+      if (j == 4 + y) par = sm;
+      float p0 = r[2], p1 = r[3], p4 = r[6], p5 = r[7];  // channels (0, 1) + 256 (2, 3) and (4, 5) + 256 (6, 7)
+      fma2(p0, p1, p0, p1, 256.0f, 256.0f, r[0], r[1]);
+      fma2(p4, p5, p4, p5, 256.0f, 256.0f, r[4], r[5]);
+      const uint32_t vw = __byte_perm(__float_as_uint(fmaf(p1, 16.0f, p0) + 8388608.0f),
+                                      __float_as_uint(fmaf(p5, 16.0f, p4) + 8388608.0f), 0x5410);
+      // a word holds both tokens of a pair: the even token's lane writes channels 0-3, the odd one's 4-7
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, 8);
+      uint8_t* unit_v = rec + kv4_v_unit_off<NG>(y, ta, j) + 8 * b1;
+      if (pair_live) {
+        *reinterpret_cast<uint32_t*>(unit_v + 4 * b0) =
+            b0 == 0 ? __byte_perm(vw, other, 0x5410) : __byte_perm(other, vw, 0x7632);
+      } else if (live) {
+        *reinterpret_cast<uint16_t*>(unit_v + 2 * b0) = (uint16_t)(vw & 0xffffu);
+        *reinterpret_cast<uint16_t*>(unit_v + 4 + 2 * b0) = (uint16_t)(vw >> 16);
+      }
+      if (live && a.v_out != nullptr) *reinterpret_cast<uint4*>(a.v_out + out + 64 * y) = kv4_values8(r, sm);
     }
-    if (live && a.v_out != nullptr)
-      *reinterpret_cast<uint4*>(a.v_out + (size_t)tok * a.Hkv * D + head + 64 * y) = kv4_values8(r, sm);
+    if (live && (j & 3) < NG)
+      *reinterpret_cast<uint32_t*>(rec + kv4_param_off<NG>(j >> 2, ta, b0, b1) + 4 * (j & 3)) = par;
+    rec += (size_t)blocks * kv4_record_bytes(D);
+    out += D;
   }
-  if (live && (j & 3) < NG)
-    *reinterpret_cast<uint32_t*>(rec + kv4_param_off<NG>(j >> 2, ta, b0, b1) + 4 * (j & 3)) = par;
 }
 
 struct Kv4GatherArgs {
@@ -237,19 +315,53 @@ struct Kv4GatherArgs {
   __nv_bfloat16* k;  // [S, Hkv, N, d]
   __nv_bfloat16* v;
   int S, Hkv, N, page_size, num_pages, max_pages;
+  int heads;  // KV heads a warp takes in turn
 };
 
-// One warp per (record, sequence): lanes as in the append, four quads of tokens in turn.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Copies a record into shared memory with the lanes of a warp, 16 bytes each.
+template <int REC>
+__device__ __forceinline__ void kv4_fetch_record(uint32_t dst, const uint8_t* src, int lane) {
+#pragma unroll
+  for (int i = 0; i < REC / 512; ++i) cp_async16(dst + i * 512 + lane * 16, src + i * 512 + lane * 16);
+  if constexpr (REC % 512 != 0) {
+    constexpr int kAt = REC / 512 * 512;
+    if (lane < (REC % 512) / 16) cp_async16(dst + kAt + lane * 16, src + kAt + lane * 16);
+  }
+}
+
 template <int NG>
-__global__ void __launch_bounds__(256) attn_kv4_gather_kernel(const __grid_constant__ Kv4GatherArgs a) {
-  constexpr int D = NG * kKv4Group;
-  const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+struct Kv4GatherCfg {
+  static constexpr int WARPS = NG == 4 ? 4 : 8;
+  static constexpr int STAGES = 2;
+};
+
+// One warp per 16 positions of a sequence and `heads` KV heads.  The work is a copy (9 d / 8 bytes
+// in and 4 d out per token and head), so what counts is loads in flight: records come in whole by
+// 16-byte asynchronous copies, the next head's while one is written out, and the lanes take their
+// codes from shared memory (lane = 8 (token of a quad) + (8-channel chunk), as in the append).
+template <int NG>
+__global__ void __launch_bounds__(Kv4GatherCfg<NG>::WARPS * 32)
+    attn_kv4_gather_kernel(const __grid_constant__ Kv4GatherArgs a) {
+  constexpr int D = NG * kKv4Group, REC = kv4_record_bytes(D);
+  using C = Kv4GatherCfg<NG>;
+  __shared__ __align__(128) uint8_t stage[C::WARPS][C::STAGES][REC];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long unit = (long long)blockIdx.x * C::WARPS + warp;
   const int nrec = (a.N + kKv4Tok - 1) / kKv4Tok;
-  const int r0 = (int)(unit % nrec);
-  const long long sh = unit / nrec;
-  const int h = (int)(sh % a.Hkv);
-  const long long sq = sh / a.Hkv;
+  const int parts = (a.Hkv + a.heads - 1) / a.heads;
+  const int h0 = (int)(unit % parts) * a.heads, h1 = min(a.Hkv, h0 + a.heads);
+  const long long sr = unit / parts;
+  const int r0 = (int)(sr % nrec);
+  const long long sq = sr / nrec;
   if (sq >= a.S) return;
   const int s = (int)sq;
   int len = __ldg(&a.seq_lens[s]);
@@ -266,33 +378,45 @@ __global__ void __launch_bounds__(256) attn_kv4_gather_kernel(const __grid_const
     return;
   }
   const int blocks = a.page_size / kKv4Tok;
-  const uint8_t* rec =
-      a.pool + (((size_t)page * a.Hkv + h) * blocks + (p0 % a.page_size) / kKv4Tok) * kv4_record_bytes(D);
+  const size_t head_bytes = (size_t)blocks * REC;
+  const uint8_t* rec = a.pool + ((size_t)page * a.Hkv + h0) * head_bytes + (size_t)((p0 % a.page_size) / kKv4Tok) * REC;
   const int i = lane >> 3, j = lane & 7, b0 = i & 1, b1 = i >> 1;
-  const size_t row0 = ((size_t)s * a.Hkv + h) * a.N + p0 + i;
+  kv4_fetch_record<REC>(smem_u32(stage[warp][0]), rec, lane);
+  cp_async_commit();
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    rec += head_bytes;
+    if (h + 1 < h1) kv4_fetch_record<REC>(smem_u32(stage[warp][(h + 1 - h0) & 1]), rec, lane);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncwarp();
+    const uint8_t* st = stage[warp][(h - h0) & 1];
+    const size_t row0 = ((size_t)s * a.Hkv + h) * a.N + p0 + i;
 #pragma unroll
-  for (int ta = 0; ta < 4; ++ta) {
-    if (p0 + 4 * ta + i >= len) break;
-    const size_t out = (row0 + 4 * ta) * D + 8 * j;
+    for (int ta = 0; ta < 4; ++ta) {
+      if (p0 + 4 * ta + i >= len) break;
+      const size_t out = (row0 + 4 * ta) * D + 8 * j;
 #pragma unroll
-    for (int y = 0; y < NG; ++y) {
-      const uint32_t ksm = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_param_off<NG>(0, ta, b0, b1) + 4 * y));
-      const uint32_t vsm = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_param_off<NG>(1, ta, b0, b1) + 4 * y));
-      const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_k_code_off(y, ta, b0, b1, j)));
-      const uint2 vu = __ldg(reinterpret_cast<const uint2*>(rec + kv4_v_unit_off<NG>(y, ta, j) + 8 * b1));
-      const uint32_t vw = __byte_perm(vu.x, vu.y, b0 == 0 ? 0x5410 : 0x7632);  // channels 0-3 | 4-7 << 16
-      float r[8];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        r[2 * c] = (float)((kw >> (4 * c)) & 15u);
-        r[2 * c + 1] = (float)((kw >> (16 + 4 * c)) & 15u);
+      for (int y = 0; y < NG; ++y) {
+        const uint32_t ksm = *reinterpret_cast<const uint32_t*>(st + kv4_param_off<NG>(0, ta, b0, b1) + 4 * y);
+        const uint32_t vsm = *reinterpret_cast<const uint32_t*>(st + kv4_param_off<NG>(1, ta, b0, b1) + 4 * y);
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(st + kv4_k_code_off(y, ta, b0, b1, j));
+        const uint2 vu = *reinterpret_cast<const uint2*>(st + kv4_v_unit_off<NG>(y, ta, j) + 8 * b1);
+        float lo[4], hi[4];
+        kv4_code_values(kw, ksm, lo, hi);  // channels 2i and 2i + 1
+        __stcs(reinterpret_cast<uint4*>(a.k + out + 64 * y),
+               make_uint4(pack_bf16x2(lo[0], hi[0]), pack_bf16x2(lo[1], hi[1]), pack_bf16x2(lo[2], hi[2]),
+                          pack_bf16x2(lo[3], hi[3])));
+        // this token's halves of the two words: channels i and 4 + i
+        kv4_code_values(__byte_perm(vu.x, vu.y, b0 == 0 ? 0x5410 : 0x7632), vsm, lo, hi);
+        __stcs(reinterpret_cast<uint4*>(a.v + out + 64 * y),
+               make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                          pack_bf16x2(hi[2], hi[3])));
       }
-      *reinterpret_cast<uint4*>(a.k + out + 64 * y) = kv4_values8(r, ksm);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) r[c] = (float)((vw >> (4 * c)) & 15u);
-      *reinterpret_cast<uint4*>(a.v + out + 64 * y) = kv4_values8(r, vsm);
     }
+    __syncwarp();  // the stage is refilled two heads later
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace attn

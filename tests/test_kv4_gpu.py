@@ -617,3 +617,19 @@ def test_binding_refusals(cuda_device):
     with pytest.raises(ab.AttnError):
         ab.attn_decode_paged_kv4(q, pool, table, n, 16, q, lse, -0.1, ws)
     assert ab.attn_get_device_status() == 0
+
+
+def test_decode_does_not_depend_on_what_shared_memory_held(cuda_device):
+    # rows that end inside a unit of two records, after calls on other data left their records behind
+    rng = np.random.default_rng(44)
+    lens = [5, 16, 17, 31, 33, 200, 1000]
+    table, num_pages = layout(rng, lens, 16)
+    pool = random_pool(rng, num_pages, 2, 16, 128)
+    q = bf16(rng, (len(lens), 8, 128))
+    o0, l0, _ = run_decode(q, pool, table, lens, 16, 0.09)
+    big_table, big_pages = layout(rng, [20000] * 4, 16)
+    for s_hi in (1e-3, 30.0, 3e4):
+        other = random_pool(rng, big_pages, 2, 16, 128, s_lo=s_hi / 2, s_hi=s_hi)
+        run_decode(bf16(rng, (4, 8, 128)), other, big_table, [20000] * 4, 16, 0.09)
+        o, lse, _ = run_decode(q, pool, table, lens, 16, 0.09)
+        assert torch.equal(o, o0) and torch.equal(lse, l0)
