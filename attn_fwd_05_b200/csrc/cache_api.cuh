@@ -40,14 +40,14 @@ attn_status launch_gather(const attn::Kv4GatherArgs& a, unsigned grid, cudaStrea
 // Launches a kernel that may be set up while the kernel before it on the stream still runs; the
 // kernel waits for that one's results itself (pdl_wait).
 template <typename... P, typename... A>
-attn_status launch_dependent(void (*k)(P...), int grid, int threads, cudaStream_t st, const A&... args) {
+attn_status launch_dependent(void (*k)(P...), dim3 grid, int threads, cudaStream_t st, const A&... args) {
   cudaLaunchAttribute attr;
   std::memset(&attr, 0, sizeof(attr));
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cfg.attrs = &attr;
@@ -86,15 +86,15 @@ attn_status launch_decode_kv4(const attn::DecKv4Args& a, cudaStream_t st, int sl
   k<<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (a.S * a.Hq <= 4 * sm_count())
-    return launch_dependent(attn::attn_decode_kv4_merge_kernel<D, NT, 16>, a.S * a.Hq, 16 * 32, st, a);
-  return launch_dependent(attn::attn_decode_kv4_merge_kernel<D, NT, 4>, a.S * a.Hq, 4 * 32, st, a);
+    return launch_dependent(attn::attn_decode_kv4_merge_kernel<D, NT, 16>, dim3(a.S * a.Hq), 16 * 32, st, a);
+  return launch_dependent(attn::attn_decode_kv4_merge_kernel<D, NT, 4>, dim3(a.S * a.Hq), 4 * 32, st, a);
 }
 
 struct PagesLayout {
-  size_t off[8], zero_bytes, total;
+  size_t off[8], zero_bytes, zero_first, total;
 };
 
-// Workspace of both page operators, in the order of the marks (cleared first) and the lists.
+// Workspace of both page operators: counts, marks (cleared by the call) and lists.
 PagesLayout pages_layout(int num_pages, int rows) {
   PagesLayout L;
   const size_t words = align256(((size_t)num_pages + 31) / 32 * 4), ids = align256((size_t)num_pages * 4),
@@ -105,7 +105,8 @@ PagesLayout pages_layout(int num_pages, int rows) {
     L.off[i] = at;
     at += sizes[i];
   }
-  L.zero_bytes = 2 * words;
+  L.zero_bytes = 256 + 2 * words;
+  L.zero_first = L.zero_bytes + ids;
   L.total = at;
   return L;
 }
@@ -128,6 +129,12 @@ attn_status pools_check(void* const* pools, int n_pools, size_t page_bytes, int 
 // CTAs that share one page copy: one for every 16 KB, up to 32.
 int copy_parts(size_t page_bytes) {
   return (int)std::max<size_t>(1, std::min<size_t>(32, page_bytes / 16384));
+}
+
+// One CTA plans the table: cheaper than a clearing, many CTAs and the wait for the last while its
+// entries take 512 threads a few rounds (measured on 4 x 71 entries: @@ us a fork against @@).
+bool small_table(int rows, int cols, int num_pages) {
+  return rows <= attn::kSmallRows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -324,7 +331,8 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   a.new_table = new_table;
   a.new_lens = new_lens;
   a.n_free = n_free;
-  a.n_list = reinterpret_cast<int*>(ws);
+  a.n_done = reinterpret_cast<int*>(ws);
+  a.n_list = reinterpret_cast<int*>(ws) + 1;
   a.full_bits = reinterpret_cast<uint32_t*>(ws + L.off[0]);
   a.part_bits = reinterpret_cast<uint32_t*>(ws + L.off[1]);
   a.first_part = reinterpret_cast<int*>(ws + L.off[2]);
@@ -339,20 +347,17 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   a.new_cols = new_max_pages;
   a.page_size = page_size;
   a.num_pages = num_pages;
-  if (cudaMemsetAsync(ws + L.off[0], 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (num_pages > 0 && cudaMemsetAsync(a.first_part, 0x7f, (size_t)num_pages * 4, st) != cudaSuccess)
-    return ATTN_ERR_CUDA;  // 0x7f7f7f7f: above every row number in use here
-  if (new_rows > 0) {
-    attn::attn_pages_fork_mark_kernel<<<(unsigned)new_rows, attn::kPagesThreads, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (small_table(new_rows, new_max_pages, num_pages)) {
+    attn::attn_pages_fork_small_kernel<<<1, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st>>>(a);
+  } else {
+    if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
   }
-  attn::attn_pages_fork_scan_kernel<<<1, attn::kScanThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (new_rows == 0) return ATTN_OK;
   const int parts = copy_parts(page_bytes);
   const dim3 grid((unsigned)new_rows, (unsigned)std::max(1, std::min(pp.n * parts, 1024)));
-  attn::attn_pages_fork_move_kernel<<<grid, attn::kPagesThreads, 0, st>>>(a, pp, parts);
-  return launch_status();
+  return launch_dependent(attn::attn_pages_fork_move_kernel, grid, attn::kPagesThreads, st, a, pp, parts);
 }
 
 attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_lens, int32_t* new_table,
@@ -384,7 +389,8 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   a.new_table = new_table;
   a.page_map = page_map;
   a.n_live = n_live;
-  a.counts = reinterpret_cast<int*>(ws);
+  a.n_done = reinterpret_cast<int*>(ws);
+  a.counts = reinterpret_cast<int*>(ws) + 1;
   a.bits = reinterpret_cast<uint32_t*>(ws + L.off[0]);
   a.prefix = reinterpret_cast<int*>(ws + L.off[1]);
   a.src = reinterpret_cast<int*>(ws + L.off[2]);
@@ -393,16 +399,15 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   a.cols = max_pages_per_seq;
   a.page_size = page_size;
   a.num_pages = num_pages;
-  if (cudaMemsetAsync(a.bits, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (num_seqs > 0) {
-    attn::attn_pages_compact_mark_kernel<<<(unsigned)num_seqs, attn::kPagesThreads, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (small_table(num_seqs, max_pages_per_seq, num_pages)) {
+    attn::attn_pages_compact_small_kernel<<<1, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4, st>>>(a);
+  } else {
+    if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);
   }
-  attn::attn_pages_compact_scan_kernel<<<1, attn::kScanThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  attn::attn_pages_compact_move_kernel<<<(unsigned)(sm_count() * 8), attn::kPagesThreads, 0, st>>>(
-      a, pp, copy_parts(page_bytes));
-  return launch_status();
+  return launch_dependent(attn::attn_pages_compact_move_kernel, dim3((unsigned)(sm_count() * 8)), attn::kPagesThreads,
+                          st, a, pp, copy_parts(page_bytes));
 }
 
 }  // extern "C"

@@ -30,6 +30,7 @@
 #pragma once
 
 #include "kv4_sm100.cuh"
+#include "pages_sm100.cuh"
 
 namespace attn {
 
@@ -85,11 +86,6 @@ __device__ __forceinline__ void mma_16816_f16_first(float (&c)[4], uint32_t a0, 
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-
-// Programmatic dependent launch: the dependent grid may be set up from here on; it waits for this
-// grid's end (and its writes) in pdl_wait.
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Transposes an 8x8 matrix of 16-bit elements held by the warp (two neighbours of a row a lane).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {

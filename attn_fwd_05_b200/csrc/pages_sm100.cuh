@@ -3,22 +3,30 @@
 //
 // The block table is the only state: a page is in use while a row of the table refers to it,
 // and free otherwise, so there is no reference count or free list to keep consistent.  Both
-// operators are three steps on one stream, with the page numbers never leaving the device:
-//   mark   the rows' pages set bits of a map over the pool (many CTAs, one row each)
-//   scan   one CTA ranks the free pages (fork) or the moves (compact) with popcounts and one
-//          block-wide scan; ranks make the result independent of the order of execution
+// operators are two kernels after one clearing of the marks, with the page numbers never leaving
+// the device:
+//   plan   the rows' pages set bits of a map over the pool (many CTAs, one row each); the CTA that
+//          finishes last ranks the free pages (fork) or the moves (compact) with popcounts and
+//          one block-wide scan.  Ranks make the result independent of the order of execution.
+//          A small table is planned by one CTA with the map in shared memory, and nothing to clear.
 //   move   many CTAs write the table and copy pages with 16-byte loads and stores
-// Integer work on a few KB is bound by the latency of the launches and of the scan; the
-// copies are bound by HBM (each byte read once and written once).
+// Integer work on a few KB is bound by the latency of the launches and of the scan (mark and scan
+// as kernels of their own, and a second clearing, cost 4 us a call more); the copies are bound by
+// HBM (each byte read once and written once).
 #pragma once
 
 #include "sm100_common.cuh"
 
 namespace attn {
 
+// Programmatic dependent launch: the dependent grid may be set up from here on; it waits for this
+// grid's end (and its writes) in pdl_wait.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr int kMaxPools = 128;     // pools that share one block table (layers x K and V)
 constexpr int kPagesThreads = 256;
-constexpr int kScanThreads = 1024;
+constexpr int kPlanThreads = 512;
 
 struct PagePools {
   uint8_t* base[kMaxPools];
@@ -35,11 +43,12 @@ struct ForkArgs {
   int32_t* new_lens;        // [rows]
   int32_t* n_free;          // [1] or null
   // workspace
+  int* n_done;              // [1] CTAs that have marked their row (cleared, as the next three)
   uint32_t* full_bits;      // [words] pages some row has as a full page
   uint32_t* part_bits;      // [words] pages some row has as its part-filled last page
-  int* first_part;          // [num_pages] lowest row with the page as its part-filled page
+  int* first_part;          // [num_pages] rows - i for the lowest row i with the page as its part-filled page
   int* free_list;           // [num_pages] free pages, ascending
-  int* row_part;            // [rows] the row's part-filled page or -1; scan: | keep flag in row_keep
+  int* row_part;            // [rows] the row's part-filled page or -1
   int* row_fresh;           // [rows] fresh pages after the part-filled one
   int* row_rank;            // [rows] rank of the row's first page from the free list
   int* row_keep;            // [rows] 1: the row keeps its part-filled page in place
@@ -47,134 +56,196 @@ struct ForkArgs {
   int S, cols, rows, new_cols, page_size, num_pages;
 };
 
-// Block-wide exclusive scan of one int per thread; *total gets the sum.  sums: 32 ints of shared
-// memory.  Every thread of a block of kScanThreads calls it.
-__device__ __forceinline__ int pages_scan(int v, int* sums, int* total) {
+// True in every thread of the CTA that arrives last, with the others' writes visible to it.
+__device__ __forceinline__ bool last_cta(int* n_done) {
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(n_done, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  __threadfence();
+  return last != 0;
+}
+
+// Block-wide exclusive scan of two ints per thread (.x and .y apart); *total gets the sums.  sums:
+// 16 pairs of shared memory.  Every thread of a block of kPlanThreads calls it.
+__device__ __forceinline__ int2 pages_scan(int2 v, int2* sums, int2* total) {
+  constexpr int W = kPlanThreads / 32;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
+  int2 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y0 = __shfl_up_sync(0xffffffffu, x.x, o), y1 = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) {
+      x.x += y0;
+      x.y += y1;
+    }
   }
-  __syncthreads();  // an earlier scan's readers of sums are done
   if (lane == 31) sums[w] = x;
   __syncthreads();
-  if (w == 0) {
-    int t = sums[lane];
+  int2 before = make_int2(x.x - v.x, x.y - v.y), all = make_int2(0, 0);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
+  for (int k = 0; k < W; ++k) {
+    const int2 s = sums[k];
+    if (k < w) {
+      before.x += s.x;
+      before.y += s.y;
     }
-    sums[lane] = t;
+    all.x += s.x;
+    all.y += s.y;
   }
-  __syncthreads();
-  *total = sums[31];
-  return (w > 0 ? sums[w - 1] : 0) + x - v;
+  *total = all;
+  return before;
 }
+
+// Tables planned by one CTA: up to this many entries, rows and pages.
+constexpr int kSmallEntries = 8192, kSmallRows = 256, kSmallPages = 65536;
 
 // ------------------------------------------------------------------ fork
 
-// One CTA per new row: its length, the entries it shares with its parent, and the marks.
-__global__ void __launch_bounds__(kPagesThreads) attn_pages_fork_mark_kernel(const __grid_constant__ ForkArgs a) {
-  const int i = blockIdx.x;
+// A new row's length, and what it takes over from its parent: {parent, full pages, part-filled last
+// page (0 or 1), new length}.
+__device__ __forceinline__ int4 fork_row(const ForkArgs& a, int i, bool* bad) {
   const int max_tokens = a.cols * a.page_size;
   int p = __ldg(&a.parents[i]), old_len = 0, new_len = 0;
-  bool bad = p < -1 || p >= a.S;
-  if (bad) p = -1;
+  const int add = a.add != nullptr ? __ldg(&a.add[i]) : 0;
+  *bad = p < -1 || p >= a.S;
+  if (*bad) p = -1;
   if (p >= 0) {
     old_len = __ldg(&a.seq_lens[p]);
     if (old_len < 0 || old_len > max_tokens) {
-      bad = true;
+      *bad = true;
       old_len = 0;
     }
-    const long long want = (long long)old_len + (a.add != nullptr ? __ldg(&a.add[i]) : 0);
+    const long long want = (long long)old_len + add;
     if (want < 0 || want > (long long)a.new_cols * a.page_size) {
-      bad = true;
+      *bad = true;
       new_len = old_len;
     } else {
       new_len = (int)want;
     }
   }
   const int kept = min(old_len, new_len);
-  const int nfull = kept / a.page_size;
-  const bool part = kept % a.page_size != 0;
-  const int32_t* src = a.table + (size_t)max(p, 0) * a.cols;
-  int32_t* dst = a.new_table + (size_t)i * a.new_cols;
-  for (int j = threadIdx.x; j < a.new_cols; j += blockDim.x) {
-    int e = -1;
-    if (j < nfull + (part ? 1 : 0)) {
-      e = __ldg(&src[j]);
-      if (e < 0 || e >= a.num_pages) {
-        latch_status(ATTN_ERR_BAD_PAGE);
-        e = -1;
-      } else if (j < nfull) {
-        atomicOr(&a.full_bits[e >> 5], 1u << (e & 31));
-      } else {
-        atomicOr(&a.part_bits[e >> 5], 1u << (e & 31));
-        atomicMin(&a.first_part[e], i);
-      }
-    }
-    dst[j] = e;
-    if (part && j == nfull) a.row_part[i] = e;
-  }
-  if (threadIdx.x == 0) {
-    if (bad) latch_status(ATTN_ERR_INVALID_ARG);
-    if (!part) a.row_part[i] = -1;
-    a.new_lens[i] = new_len;
-    a.row_fresh[i] = (new_len + a.page_size - 1) / a.page_size - nfull - (part ? 1 : 0);
-  }
+  return make_int4(p, kept / a.page_size, kept % a.page_size != 0 ? 1 : 0, new_len);
 }
 
-// One CTA: the free pages in ascending order, and which of them each row gets.
-__global__ void __launch_bounds__(kScanThreads) attn_pages_fork_scan_kernel(const __grid_constant__ ForkArgs a) {
-  __shared__ int sums[32];
+// Entry j of new row i: the parent's page (marked in the maps) or -1.
+__device__ __forceinline__ void fork_entry(const ForkArgs& a, int i, int j, int4 row, uint32_t* full, uint32_t* part,
+                                           int* first_part) {
+  int e = -1;
+  if (j < row.y + row.z) {
+    e = __ldg(&a.table[(size_t)row.x * a.cols + j]);
+    if (e < 0 || e >= a.num_pages) {
+      latch_status(ATTN_ERR_BAD_PAGE);
+      e = -1;
+    } else if (j < row.y) {
+      atomicOr(&full[e >> 5], 1u << (e & 31));
+    } else {
+      atomicOr(&part[e >> 5], 1u << (e & 31));
+      if (first_part != nullptr) atomicMax(&first_part[e], a.rows - i);
+    }
+    if (j == row.y) a.row_part[i] = e;
+  }
+  a.new_table[(size_t)i * a.new_cols + j] = e;
+}
+
+__device__ __forceinline__ void fork_row_done(const ForkArgs& a, int i, int4 row, bool bad) {
+  if (bad) latch_status(ATTN_ERR_INVALID_ARG);
+  if (row.z == 0) a.row_part[i] = -1;
+  a.new_lens[i] = row.w;
+  a.row_fresh[i] = (row.w + a.page_size - 1) / a.page_size - row.y - row.z;
+}
+
+// Lists the free pages in ascending order and gives each row its rank in that list.  lowest(i, e): row
+// i is the lowest with the part-filled page e.  Such a page stays with the lowest row that has it,
+// unless some row has it as a full page (that row's tokens must not be written over).
+template <typename Lowest>
+__device__ __forceinline__ void fork_rank(const ForkArgs& a, const volatile uint32_t* full, const volatile uint32_t* part,
+                                          Lowest lowest, int2* sums) {
   const int tid = threadIdx.x;
   const int words = (a.num_pages + 31) / 32;
-  const int wpt = (words + kScanThreads - 1) / kScanThreads;
+  const int wpt = (words + kPlanThreads - 1) / kPlanThreads;
+  const int w0 = min(words, tid * wpt), w1 = min(words, w0 + wpt);
   auto free_bits = [&](int w) -> uint32_t {
-    uint32_t f = ~(a.full_bits[w] | a.part_bits[w]);
+    uint32_t f = ~(full[w] | part[w]);
     if (w == words - 1 && (a.num_pages & 31) != 0) f &= (1u << (a.num_pages & 31)) - 1u;
     return f;
   };
-  int mine = 0;
-  for (int w = tid * wpt; w < min(words, (tid + 1) * wpt); ++w) mine += __popc(free_bits(w));
-  int n_free;
-  int rank = pages_scan(mine, sums, &n_free);
-  for (int w = tid * wpt; w < min(words, (tid + 1) * wpt); ++w) {
-    uint32_t f = free_bits(w);
-    while (f != 0) {
-      const int b = __ffs(f) - 1;
-      a.free_list[rank++] = 32 * w + b;
-      f &= f - 1;
-    }
-  }
-  // rows in order: a part-filled page stays with the lowest row that has it, unless some row has it
-  // as a full page (that row's tokens must not be written over)
-  const int rpt = (a.rows + kScanThreads - 1) / kScanThreads;
-  int need = 0;
-  for (int i = tid * rpt; i < min(a.rows, (tid + 1) * rpt); ++i) {
-    const int e = a.row_part[i];
+  const volatile int *row_part = a.row_part, *row_fresh = a.row_fresh;
+  const int rpt = (a.rows + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = min(a.rows, tid * rpt), i1 = min(a.rows, i0 + rpt);
+  int2 mine = make_int2(0, 0);  // free pages, pages needed
+  for (int w = w0; w < w1; ++w) mine.x += __popc(free_bits(w));
+  for (int i = i0; i < i1; ++i) {
+    const int e = row_part[i];
     int keep = 0;
     if (e >= 0) {
-      keep = a.first_part[e] == i && (a.full_bits[e >> 5] >> (e & 31) & 1u) == 0;
-      need += 1 - keep;
+      keep = lowest(i, e) && (full[e >> 5] >> (e & 31) & 1u) == 0;
+      mine.y += 1 - keep;
     }
     a.row_keep[i] = keep;
-    need += a.row_fresh[i];
+    mine.y += row_fresh[i];
   }
-  int total;
-  int at = pages_scan(need, sums, &total);
-  for (int i = tid * rpt; i < min(a.rows, (tid + 1) * rpt); ++i) {
-    a.row_rank[i] = at;
-    at += a.row_fresh[i] + (a.row_part[i] >= 0 && !a.row_keep[i] ? 1 : 0);
+  int2 total;
+  int2 at = pages_scan(mine, sums, &total);
+  for (int w = w0; w < w1; ++w)
+    for (uint32_t f = free_bits(w); f != 0; f &= f - 1) a.free_list[at.x++] = 32 * w + __ffs(f) - 1;
+  for (int i = i0; i < i1; ++i) {
+    a.row_rank[i] = at.y;
+    at.y += row_fresh[i] + (row_part[i] >= 0 && !a.row_keep[i] ? 1 : 0);
   }
   if (tid == 0) {
-    if (total > n_free) latch_status(ATTN_ERR_TOO_LARGE);
-    *a.n_list = n_free;
-    if (a.n_free != nullptr) *a.n_free = max(0, n_free - total);
+    if (total.y > total.x) latch_status(ATTN_ERR_TOO_LARGE);
+    *a.n_list = total.x;
+    if (a.n_free != nullptr) *a.n_free = max(0, total.x - total.y);
   }
+}
+
+// One CTA per new row (one at least); the last one to finish ranks.
+__global__ void __launch_bounds__(kPlanThreads) attn_pages_fork_plan_kernel(const __grid_constant__ ForkArgs a) {
+  __shared__ int2 sums[kPlanThreads / 32];
+  const int i = blockIdx.x;
+  if (i < a.rows) {
+    bool bad;
+    const int4 row = fork_row(a, i, &bad);
+    for (int j = threadIdx.x; j < a.new_cols; j += kPlanThreads)
+      fork_entry(a, i, j, row, a.full_bits, a.part_bits, a.first_part);
+    if (threadIdx.x == 0) fork_row_done(a, i, row, bad);
+  }
+  if (!last_cta(a.n_done)) return;
+  const volatile int* first_part = a.first_part;
+  fork_rank(a, a.full_bits, a.part_bits, [&](int r, int e) { return first_part[e] == a.rows - r; }, sums);
+}
+
+// The whole plan of a small table in one CTA; dynamic shared memory holds the two maps.
+__global__ void __launch_bounds__(kPlanThreads) attn_pages_fork_small_kernel(const __grid_constant__ ForkArgs a) {
+  extern __shared__ uint32_t maps[];
+  __shared__ int2 sums[kPlanThreads / 32];
+  __shared__ int4 rows[kSmallRows];
+  const int words = (a.num_pages + 31) / 32;
+  uint32_t *full = maps, *part = maps + words;
+  for (int w = threadIdx.x; w < 2 * words; w += kPlanThreads) maps[w] = 0;
+  if (threadIdx.x < a.rows) {
+    bool bad;
+    const int4 row = fork_row(a, threadIdx.x, &bad);
+    rows[threadIdx.x] = row;
+    fork_row_done(a, threadIdx.x, row, bad);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.rows * a.new_cols; k += kPlanThreads) {
+    const int i = k / a.new_cols;
+    fork_entry(a, i, k % a.new_cols, rows[i], full, part, nullptr);
+  }
+  __syncthreads();  // orders the block's global writes of row_part before their reads, too
+  const volatile int* row_part = a.row_part;
+  if (threadIdx.x < a.rows) rows[threadIdx.x].x = row_part[threadIdx.x];
+  __syncthreads();
+  auto lowest = [&](int r, int e) {
+    for (int k = 0; k < r; ++k)
+      if (rows[k].x == e) return false;
+    return true;
+  };
+  fork_rank(a, full, part, lowest, sums);
 }
 
 // Copies `bytes` (a multiple of 16) with the block's threads, part `part` of `parts`.
@@ -197,6 +268,7 @@ __device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, lon
 // CTA (row, pool x part): the row's fresh entries (first CTA of a row) and its page copy.
 __global__ void __launch_bounds__(kPagesThreads)
     attn_pages_fork_move_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PagePools pools, int parts) {
+  pdl_wait();
   const int i = blockIdx.x;
   const int rank = a.row_rank[i], e = a.row_part[i], n_list = *a.n_list;
   const bool copies = e >= 0 && !a.row_keep[i];
@@ -227,6 +299,7 @@ struct CompactArgs {
   int32_t* page_map;        // [num_pages]
   int32_t* n_live;          // [1] or null
   // workspace
+  int* n_done;              // [1] CTAs that have marked their row (cleared, as the next)
   uint32_t* bits;           // [words] pages in use
   int* prefix;              // [words] pages in use before the word
   int* src;                 // [num_pages] pages that move, ascending
@@ -241,57 +314,89 @@ __device__ __forceinline__ int pages_of_row(const CompactArgs& a, int s, bool* b
   return *bad ? 0 : (len + a.page_size - 1) / a.page_size;
 }
 
-__global__ void __launch_bounds__(kPagesThreads) attn_pages_compact_mark_kernel(const __grid_constant__ CompactArgs a) {
-  const int s = blockIdx.x;
-  bool bad;
-  const int n = pages_of_row(a, s, &bad);
-  if (bad && threadIdx.x == 0) latch_status(ATTN_ERR_INVALID_ARG);
-  for (int j = threadIdx.x; j < n; j += blockDim.x) {
-    const int e = a.table[(size_t)s * a.cols + j];
-    if (e < 0 || e >= a.num_pages)
-      latch_status(ATTN_ERR_BAD_PAGE);
-    else
-      atomicOr(&a.bits[e >> 5], 1u << (e & 31));
-  }
-}
-
-// One CTA: with n pages in use, page ids below n stay and the others move, in ascending order,
-// into the free ids below n.  No page is both a source and a destination.
-__global__ void __launch_bounds__(kScanThreads) attn_pages_compact_scan_kernel(const __grid_constant__ CompactArgs a) {
-  __shared__ int sums[32];
+// With n pages in use, page ids below n stay and the others move, in ascending order, into the free
+// ids below n.  No page is both a source and a destination.  A mover's rank is the number of pages in
+// use before it, less those that stay; a hole's is the number of free ids before it.
+__device__ __forceinline__ void compact_rank(const CompactArgs& a, const volatile uint32_t* bits, int2* sums) {
+  __shared__ int stay;
   const int tid = threadIdx.x;
   const int words = (a.num_pages + 31) / 32;
-  const int wpt = (words + kScanThreads - 1) / kScanThreads;
-  const int w0 = min(words, tid * wpt), w1 = min(words, (tid + 1) * wpt);
+  const int wpt = (words + kPlanThreads - 1) / kPlanThreads;
+  const int w0 = min(words, tid * wpt), w1 = min(words, w0 + wpt);
+  if (tid == 0) stay = 0;
   int mine = 0;
-  for (int w = w0; w < w1; ++w) mine += __popc(a.bits[w]);
-  int live;
-  int before = pages_scan(mine, sums, &live);
+  for (int w = w0; w < w1; ++w) mine += __popc(bits[w]);
+  int2 total;
+  const int first = pages_scan(make_int2(mine, 0), sums, &total).x;
+  const int live = total.x;
   auto below = [&](int w) -> uint32_t {  // mask of the word's ids below `live`
     const int d = live - 32 * w;
     return d >= 32 ? 0xffffffffu : (d <= 0 ? 0u : (1u << d) - 1u);
   };
-  int movers = 0;
+  int before = first;
   for (int w = w0; w < w1; ++w) {
+    const uint32_t b = bits[w];
+    a.bits[w] = b;
     a.prefix[w] = before;
-    before += __popc(a.bits[w]);
-    movers += __popc(a.bits[w] & ~below(w));
+    if (live / 32 == w) stay = before + __popc(b & below(w));
+    before += __popc(b);
   }
-  int n_move;
-  int ms = pages_scan(movers, sums, &n_move);
-  int holes = 0;
-  for (int w = w0; w < w1; ++w) holes += __popc(~a.bits[w] & below(w));
-  int n_holes;
-  int hs = pages_scan(holes, sums, &n_holes);  // as many as movers
+  if (tid == 0 && live / 32 == words) stay = live;  // every page of a pool of 32 k pages is in use
+  __syncthreads();
+  before = first;
   for (int w = w0; w < w1; ++w) {
-    for (uint32_t f = a.bits[w] & ~below(w); f != 0; f &= f - 1) a.src[ms++] = 32 * w + __ffs(f) - 1;
-    for (uint32_t f = ~a.bits[w] & below(w); f != 0; f &= f - 1) a.dst[hs++] = 32 * w + __ffs(f) - 1;
+    const uint32_t b = bits[w];
+    int r = before - stay + __popc(b & below(w));
+    for (uint32_t f = b & ~below(w); f != 0; f &= f - 1) a.src[r++] = 32 * w + __ffs(f) - 1;
+    r = 32 * w - before;
+    for (uint32_t f = ~b & below(w); f != 0; f &= f - 1) a.dst[r++] = 32 * w + __ffs(f) - 1;
+    before += __popc(b);
   }
   if (tid == 0) {
     a.counts[0] = live;
-    a.counts[1] = n_move;
+    a.counts[1] = live - stay;
     if (a.n_live != nullptr) *a.n_live = live;
   }
+}
+
+__device__ __forceinline__ void compact_mark(const CompactArgs& a, int s, int j, uint32_t* bits) {
+  const int e = a.table[(size_t)s * a.cols + j];
+  if (e < 0 || e >= a.num_pages)
+    latch_status(ATTN_ERR_BAD_PAGE);
+  else
+    atomicOr(&bits[e >> 5], 1u << (e & 31));
+}
+
+// One CTA per row (one at least) marks its pages; the last one to finish ranks.
+__global__ void __launch_bounds__(kPlanThreads) attn_pages_compact_plan_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ int2 sums[kPlanThreads / 32];
+  if (blockIdx.x < a.S) {
+    bool bad;
+    const int n = pages_of_row(a, blockIdx.x, &bad);
+    if (bad && threadIdx.x == 0) latch_status(ATTN_ERR_INVALID_ARG);
+    for (int j = threadIdx.x; j < n; j += kPlanThreads) compact_mark(a, blockIdx.x, j, a.bits);
+  }
+  if (!last_cta(a.n_done)) return;
+  compact_rank(a, a.bits, sums);
+}
+
+// The whole plan of a small table in one CTA; dynamic shared memory holds the map.
+__global__ void __launch_bounds__(kPlanThreads) attn_pages_compact_small_kernel(const __grid_constant__ CompactArgs a) {
+  extern __shared__ uint32_t maps[];
+  __shared__ int2 sums[kPlanThreads / 32];
+  __shared__ int used[kSmallRows];
+  const int words = (a.num_pages + 31) / 32;
+  for (int w = threadIdx.x; w < words; w += kPlanThreads) maps[w] = 0;
+  if (threadIdx.x < a.S) {
+    bool bad;
+    used[threadIdx.x] = pages_of_row(a, threadIdx.x, &bad);
+    if (bad) latch_status(ATTN_ERR_INVALID_ARG);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.S * a.cols; k += kPlanThreads)
+    if (k % a.cols < used[k / a.cols]) compact_mark(a, k / a.cols, k % a.cols, maps);
+  __syncthreads();
+  compact_rank(a, maps, sums);
 }
 
 // The new number of page e in use.  Movers are ranked by the pages in use before them: of those,
@@ -306,6 +411,7 @@ __device__ __forceinline__ int compact_to(const CompactArgs& a, int e, int live,
 __global__ void __launch_bounds__(kPagesThreads)
     attn_pages_compact_move_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PagePools pools,
                                    int parts) {
+  pdl_wait();
   const int live = a.counts[0], n_move = a.counts[1];
   const long long step = (long long)gridDim.x * blockDim.x;
   const long long t0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
