@@ -131,10 +131,30 @@ int copy_parts(size_t page_bytes) {
   return (int)std::max<size_t>(1, std::min<size_t>(32, page_bytes / 16384));
 }
 
-// One CTA plans the table: cheaper than a clearing, many CTAs and the wait for the last while its
-// entries take 512 threads a few rounds (measured on 4 x 71 entries: @@ us a fork against @@).
-bool small_table(int rows, int cols, int num_pages) {
-  return rows <= attn::kSmallRows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages;
+// One launch of one cluster: cheaper than a clearing and two kernels while one CTA plans the entries
+// in a few rounds and 8 CTAs copy what there can be to copy in a few microseconds.
+bool small_table(int rows, int cols, int num_pages, double copies, const attn::PagePools& pp) {
+  return rows <= attn::kSmallRows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages &&
+         copies * pp.n * (double)pp.page_bytes <= (double)attn::kSmallBytes;
+}
+
+// Launches one cluster of kSmallCluster CTAs.
+template <typename... P, typename... A>
+attn_status launch_cluster(void (*k)(P...), int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attn::kSmallCluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(attn::kSmallCluster);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...) == cudaSuccess ? launch_status() : ATTN_ERR_CUDA;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -347,15 +367,14 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   a.new_cols = new_max_pages;
   a.page_size = page_size;
   a.num_pages = num_pages;
-  if (small_table(new_rows, new_max_pages, num_pages)) {
-    attn::attn_pages_fork_small_kernel<<<1, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st>>>(a);
-  } else {
-    if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
-    attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
-  }
+  const int parts = copy_parts(page_bytes);
+  if (small_table(new_rows, new_max_pages, num_pages, new_rows, pp))
+    return launch_cluster(attn::attn_pages_fork_small_kernel, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st,
+                          a, pp);
+  if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
+  attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (new_rows == 0) return ATTN_OK;
-  const int parts = copy_parts(page_bytes);
   const dim3 grid((unsigned)new_rows, (unsigned)std::max(1, std::min(pp.n * parts, 1024)));
   return launch_dependent(attn::attn_pages_fork_move_kernel, grid, attn::kPagesThreads, st, a, pp, parts);
 }
@@ -399,15 +418,16 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   a.cols = max_pages_per_seq;
   a.page_size = page_size;
   a.num_pages = num_pages;
-  if (small_table(num_seqs, max_pages_per_seq, num_pages)) {
-    attn::attn_pages_compact_small_kernel<<<1, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4, st>>>(a);
-  } else {
-    if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
-    attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);
-  }
+  const int parts = copy_parts(page_bytes);
+  // a page moves into a free one, so at most half of the pool moves
+  if (small_table(num_seqs, max_pages_per_seq, num_pages, std::min((double)num_seqs * max_pages_per_seq, num_pages / 2.0), pp))
+    return launch_cluster(attn::attn_pages_compact_small_kernel, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4,
+                          st, a, pp);
+  if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
+  attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   return launch_dependent(attn::attn_pages_compact_move_kernel, dim3((unsigned)(sm_count() * 8)), attn::kPagesThreads,
-                          st, a, pp, copy_parts(page_bytes));
+                          st, a, pp, parts);
 }
 
 }  // extern "C"

@@ -138,12 +138,16 @@ __device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8])
     r[2 * i] = q0;
     r[2 * i + 1] = q1;
   }
-  // magnitudes order like their bits; a zero becomes the largest
-  const uint32_t least = min_u16x2(min_u16x2(magnitude_less_one(w[0]), magnitude_less_one(w[1])),
-                                   min_u16x2(magnitude_less_one(w[2]), magnitude_less_one(w[3])));
-  const uint32_t small = __float_as_uint(s * 0.000244140625f) >> 16;  // 2^-12 s
-  const bool fine = plain && min(least & 0xffffu, least >> 16) >= small &&
-                    ((__float_as_uint(lo) >> 16) & 0x7fffu) - 1u >= small;
+  // the least magnitude, zeros included, settles it nearly always; else the least one that is not 0
+  // (magnitudes order like their bits, and less one a zero becomes the largest)
+  const __nv_bfloat162 least2 = __hmin2(__hmin2(__habs2(h[0]), __habs2(h[1])), __hmin2(__habs2(h[2]), __habs2(h[3])));
+  const float tiny = s * 0.000244140625f;  // 2^-12 s
+  bool fine = plain && (fabsf(lo) >= tiny || lo == 0.0f);
+  if (fminf(__low2float(least2), __high2float(least2)) < tiny) {
+    const uint32_t least = min_u16x2(min_u16x2(magnitude_less_one(w[0]), magnitude_less_one(w[1])),
+                                     min_u16x2(magnitude_less_one(w[2]), magnitude_less_one(w[3])));
+    fine = fine && min(least & 0xffffu, least >> 16) >= __float_as_uint(tiny) >> 16;
+  }
   if (span == 0.0f) {  // a constant group, or a token that is not there
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = 0.0f;

@@ -8,7 +8,8 @@
 //   plan   the rows' pages set bits of a map over the pool (many CTAs, one row each); the CTA that
 //          finishes last ranks the free pages (fork) or the moves (compact) with popcounts and
 //          one block-wide scan.  Ranks make the result independent of the order of execution.
-//          A small table is planned by one CTA with the map in shared memory, and nothing to clear.
+//          A small table is planned and moved in one launch by one cluster, with the map in shared
+//          memory and nothing to clear.
 //   move   many CTAs write the table and copy pages with 16-byte loads and stores
 // Integer work on a few KB is bound by the latency of the launches and of the scan (mark and scan
 // as kernels of their own, and a second clearing, cost 4 us a call more); the copies are bound by
@@ -56,6 +57,11 @@ struct ForkArgs {
   int S, cols, rows, new_cols, page_size, num_pages;
 };
 
+// Barrier of the cluster's CTAs; what they wrote to global memory before it is visible after it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // True in every thread of the CTA that arrives last, with the others' writes visible to it.
 __device__ __forceinline__ bool last_cta(int* n_done) {
   __shared__ int last;
@@ -98,8 +104,9 @@ __device__ __forceinline__ int2 pages_scan(int2 v, int2* sums, int2* total) {
   return before;
 }
 
-// Tables planned by one CTA: up to this many entries, rows and pages.
-constexpr int kSmallEntries = 8192, kSmallRows = 256, kSmallPages = 65536;
+// Tables handled by one cluster: up to this many entries, rows and pages, and bytes to copy at most.
+constexpr int kSmallEntries = 8192, kSmallRows = 256, kSmallPages = 65536, kSmallCluster = 8;
+constexpr long long kSmallBytes = 8ll << 20;
 
 // ------------------------------------------------------------------ fork
 
@@ -217,37 +224,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_pages_fork_plan_kernel(cons
   fork_rank(a, a.full_bits, a.part_bits, [&](int r, int e) { return first_part[e] == a.rows - r; }, sums);
 }
 
-// The whole plan of a small table in one CTA; dynamic shared memory holds the two maps.
-__global__ void __launch_bounds__(kPlanThreads) attn_pages_fork_small_kernel(const __grid_constant__ ForkArgs a) {
-  extern __shared__ uint32_t maps[];
-  __shared__ int2 sums[kPlanThreads / 32];
-  __shared__ int4 rows[kSmallRows];
-  const int words = (a.num_pages + 31) / 32;
-  uint32_t *full = maps, *part = maps + words;
-  for (int w = threadIdx.x; w < 2 * words; w += kPlanThreads) maps[w] = 0;
-  if (threadIdx.x < a.rows) {
-    bool bad;
-    const int4 row = fork_row(a, threadIdx.x, &bad);
-    rows[threadIdx.x] = row;
-    fork_row_done(a, threadIdx.x, row, bad);
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < a.rows * a.new_cols; k += kPlanThreads) {
-    const int i = k / a.new_cols;
-    fork_entry(a, i, k % a.new_cols, rows[i], full, part, nullptr);
-  }
-  __syncthreads();  // orders the block's global writes of row_part before their reads, too
-  const volatile int* row_part = a.row_part;
-  if (threadIdx.x < a.rows) rows[threadIdx.x].x = row_part[threadIdx.x];
-  __syncthreads();
-  auto lowest = [&](int r, int e) {
-    for (int k = 0; k < r; ++k)
-      if (rows[k].x == e) return false;
-    return true;
-  };
-  fork_rank(a, full, part, lowest, sums);
-}
-
 // Copies `bytes` (a multiple of 16) with the block's threads, part `part` of `parts`.
 __device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, long long bytes, int part, int parts) {
   const long long n = bytes / 16;
@@ -265,28 +241,101 @@ __device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, lon
   for (; i < hi; i += kPagesThreads) __stcs(d + i, __ldcs(s + i));
 }
 
-// CTA (row, pool x part): the row's fresh entries (first CTA of a row) and its page copy.
+// Pieces of a page that a warp copies, all their loads in flight at once.
+constexpr int kPieceBytes = 4096;
+
+__device__ __forceinline__ void copy_piece(const PagePools& pools, int pool, int src, int dst, int piece) {
+  const int lane = threadIdx.x & 31;
+  const long long n = min((long long)kPieceBytes, pools.page_bytes - (long long)piece * kPieceBytes) / 16;
+  uint8_t* base = pools.base[pool] + (long long)piece * kPieceBytes;
+  const uint4* s = reinterpret_cast<const uint4*>(base + (size_t)src * pools.page_bytes);
+  uint4* d = reinterpret_cast<uint4*>(base + (size_t)dst * pools.page_bytes);
+  uint4 v[kPieceBytes / 512];
+#pragma unroll
+  for (int k = 0; k < kPieceBytes / 512; ++k)
+    if (lane + 32 * k < n) v[k] = __ldcs(s + lane + 32 * k);
+#pragma unroll
+  for (int k = 0; k < kPieceBytes / 512; ++k)
+    if (lane + 32 * k < n) __stcs(d + lane + 32 * k, v[k]);
+}
+
+__device__ __forceinline__ int pieces_of(const PagePools& pools) {
+  return (int)((pools.page_bytes + kPieceBytes - 1) / kPieceBytes);
+}
+
+// A planned row's page to copy from (.x) and to (.y, -1: nothing to copy).
+__device__ __forceinline__ int2 fork_copy(const ForkArgs& a, int i, int n_list) {
+  const int rank = a.row_rank[i], e = a.row_part[i];
+  return make_int2(e, e >= 0 && !a.row_keep[i] && rank < n_list ? a.free_list[rank] : -1);
+}
+
+// The entries of row i that come from the free pages.
+__device__ __forceinline__ void fork_fresh(const ForkArgs& a, int i, int n_list, int thread, int threads) {
+  const int rank = a.row_rank[i], fresh = a.row_fresh[i];
+  const bool copies = a.row_part[i] >= 0 && !a.row_keep[i];
+  const int first = (a.new_lens[i] + a.page_size - 1) / a.page_size - fresh;
+  int32_t* row = a.new_table + (size_t)i * a.new_cols;
+  if (copies && thread == 0) row[first - 1] = rank < n_list ? a.free_list[rank] : -1;
+  const int r0 = rank + (copies ? 1 : 0);
+  for (int j = thread; j < fresh; j += threads) row[first + j] = r0 + j < n_list ? a.free_list[r0 + j] : -1;
+}
+
+// CTA (row, pool x part).
 __global__ void __launch_bounds__(kPagesThreads)
     attn_pages_fork_move_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PagePools pools, int parts) {
   pdl_wait();
-  const int i = blockIdx.x;
-  const int rank = a.row_rank[i], e = a.row_part[i], n_list = *a.n_list;
-  const bool copies = e >= 0 && !a.row_keep[i];
-  const int to = copies && rank < n_list ? a.free_list[rank] : -1;
-  if (blockIdx.y == 0) {
-    const int len = a.new_lens[i];
-    const int fresh = a.row_fresh[i];
-    const int first = (len + a.page_size - 1) / a.page_size - fresh;
-    int32_t* row = a.new_table + (size_t)i * a.new_cols;
-    if (copies && threadIdx.x == 0) row[first - 1] = to;
-    const int r0 = rank + (copies ? 1 : 0);
-    for (int j = threadIdx.x; j < fresh; j += blockDim.x) row[first + j] = r0 + j < n_list ? a.free_list[r0 + j] : -1;
-  }
-  if (to < 0) return;
+  const int i = blockIdx.x, n_list = *a.n_list;
+  if (blockIdx.y == 0) fork_fresh(a, i, n_list, threadIdx.x, kPagesThreads);
+  const int2 c = fork_copy(a, i, n_list);
+  if (c.y < 0) return;
   for (int w = blockIdx.y; w < pools.n * parts; w += gridDim.y) {
     uint8_t* base = pools.base[w / parts];
-    copy_bytes(base + (size_t)to * pools.page_bytes, base + (size_t)e * pools.page_bytes, pools.page_bytes, w % parts,
+    copy_bytes(base + (size_t)c.y * pools.page_bytes, base + (size_t)c.x * pools.page_bytes, pools.page_bytes, w % parts,
                parts);
+  }
+}
+
+// A small table in one launch of one cluster: its first CTA plans with the maps in (dynamic) shared
+// memory while the others wait at the cluster's barrier, then all of them move.
+__global__ void __launch_bounds__(kPlanThreads)
+    attn_pages_fork_small_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PagePools pools) {
+  extern __shared__ uint32_t maps[];
+  __shared__ int2 sums[kPlanThreads / 32];
+  __shared__ int4 rows[kSmallRows];
+  if (blockIdx.x == 0) {
+    const int words = (a.num_pages + 31) / 32;
+    uint32_t *full = maps, *part = maps + words;
+    for (int w = threadIdx.x; w < 2 * words; w += kPlanThreads) maps[w] = 0;
+    if (threadIdx.x < a.rows) {
+      bool bad;
+      const int4 row = fork_row(a, threadIdx.x, &bad);
+      rows[threadIdx.x] = row;
+      fork_row_done(a, threadIdx.x, row, bad);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.rows * a.new_cols; k += kPlanThreads) {
+      const int i = k / a.new_cols;
+      fork_entry(a, i, k % a.new_cols, rows[i], full, part, nullptr);
+    }
+    __syncthreads();  // orders the block's global writes of row_part before their reads, too
+    const volatile int* row_part = a.row_part;
+    if (threadIdx.x < a.rows) rows[threadIdx.x].x = row_part[threadIdx.x];
+    __syncthreads();
+    auto lowest = [&](int r, int e) {
+      for (int k = 0; k < r; ++k)
+        if (rows[k].x == e) return false;
+      return true;
+    };
+    fork_rank(a, full, part, lowest, sums);
+  }
+  cluster_barrier();
+  const int warp = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kPlanThreads / 32);
+  const int n_list = *a.n_list;
+  for (int i = warp; i < a.rows; i += warps) fork_fresh(a, i, n_list, threadIdx.x & 31, 32);
+  const int pieces = pieces_of(pools), each = pools.n * pieces;
+  for (int k = warp; k < a.rows * each; k += warps) {
+    const int2 c = fork_copy(a, k / each, n_list);
+    if (c.y >= 0) copy_piece(pools, k % each / pieces, c.x, c.y, k % pieces);
   }
 }
 
@@ -380,25 +429,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_pages_compact_plan_kernel(c
   compact_rank(a, a.bits, sums);
 }
 
-// The whole plan of a small table in one CTA; dynamic shared memory holds the map.
-__global__ void __launch_bounds__(kPlanThreads) attn_pages_compact_small_kernel(const __grid_constant__ CompactArgs a) {
-  extern __shared__ uint32_t maps[];
-  __shared__ int2 sums[kPlanThreads / 32];
-  __shared__ int used[kSmallRows];
-  const int words = (a.num_pages + 31) / 32;
-  for (int w = threadIdx.x; w < words; w += kPlanThreads) maps[w] = 0;
-  if (threadIdx.x < a.S) {
-    bool bad;
-    used[threadIdx.x] = pages_of_row(a, threadIdx.x, &bad);
-    if (bad) latch_status(ATTN_ERR_INVALID_ARG);
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < a.S * a.cols; k += kPlanThreads)
-    if (k % a.cols < used[k / a.cols]) compact_mark(a, k / a.cols, k % a.cols, maps);
-  __syncthreads();
-  compact_rank(a, maps, sums);
-}
-
 // The new number of page e in use.  Movers are ranked by the pages in use before them: of those,
 // live - n_move stay.
 __device__ __forceinline__ int compact_to(const CompactArgs& a, int e, int live, int n_move) {
@@ -407,12 +437,8 @@ __device__ __forceinline__ int compact_to(const CompactArgs& a, int e, int live,
   return a.dst[r];
 }
 
-// Grid-stride over the table, the map and the pages to move.
-__global__ void __launch_bounds__(kPagesThreads)
-    attn_pages_compact_move_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PagePools pools,
-                                   int parts) {
-  pdl_wait();
-  const int live = a.counts[0], n_move = a.counts[1];
+// Writes the table and the map, grid-stride.
+__device__ __forceinline__ void compact_write(const CompactArgs& a, int live, int n_move) {
   const long long step = (long long)gridDim.x * blockDim.x;
   const long long t0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   for (long long i = t0; i < a.num_pages; i += step) {
@@ -430,6 +456,14 @@ __global__ void __launch_bounds__(kPagesThreads)
     }
     a.new_table[i] = to;
   }
+}
+
+__global__ void __launch_bounds__(kPagesThreads)
+    attn_pages_compact_move_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PagePools pools,
+                                   int parts) {
+  pdl_wait();
+  const int live = a.counts[0], n_move = a.counts[1];
+  compact_write(a, live, n_move);
   const long long work = (long long)n_move * pools.n * parts;
   for (long long w = blockIdx.x; w < work; w += gridDim.x) {
     const int part = (int)(w % parts);
@@ -439,6 +473,35 @@ __global__ void __launch_bounds__(kPagesThreads)
     copy_bytes(base + (size_t)a.dst[k] * pools.page_bytes, base + (size_t)a.src[k] * pools.page_bytes,
                pools.page_bytes, part, parts);
   }
+}
+
+// A small table in one launch of one cluster, as for the fork.
+__global__ void __launch_bounds__(kPlanThreads)
+    attn_pages_compact_small_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PagePools pools) {
+  extern __shared__ uint32_t maps[];
+  __shared__ int2 sums[kPlanThreads / 32];
+  __shared__ int used[kSmallRows];
+  if (blockIdx.x == 0) {
+    const int words = (a.num_pages + 31) / 32;
+    for (int w = threadIdx.x; w < words; w += kPlanThreads) maps[w] = 0;
+    if (threadIdx.x < a.S) {
+      bool bad;
+      used[threadIdx.x] = pages_of_row(a, threadIdx.x, &bad);
+      if (bad) latch_status(ATTN_ERR_INVALID_ARG);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.S * a.cols; k += kPlanThreads)
+      if (k % a.cols < used[k / a.cols]) compact_mark(a, k / a.cols, k % a.cols, maps);
+    __syncthreads();
+    compact_rank(a, maps, sums);
+  }
+  cluster_barrier();
+  const int live = a.counts[0], n_move = a.counts[1];
+  compact_write(a, live, n_move);
+  const int warp = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kPlanThreads / 32);
+  const int pieces = pieces_of(pools), each = pools.n * pieces;
+  for (int k = warp; k < n_move * each; k += warps)
+    copy_piece(pools, k % each / pieces, a.src[k / each], a.dst[k / each], k % pieces);
 }
 
 }  // namespace attn
