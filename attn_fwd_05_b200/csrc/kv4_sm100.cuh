@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t magnitude_less_one(uint32_t w) {
 }
 
 // One lane's 8 channels of a group whose 64 channels lie in 8 neighbouring lanes: the group's
-// scale and minimum (packed s | m << 16) and the codes as floats in r[0..7].
+// scale and minimum, and the codes as floats.
 //
 // c = nearest integer to (x - m) / s, ties to even, of the exact quotient.  Values of few
 // significant bits meet a border k + 1/2 between two codes often, so borders have to be exact on
@@ -91,75 +91,108 @@ __device__ __forceinline__ uint32_t magnitude_less_one(uint32_t w) {
 //
 // The scale's division by 15 is a product with 1/15 and one correction by its remainder, which
 // gives the correctly rounded quotient for every 24-bit significand (checked exhaustively).
-__device__ __forceinline__ uint32_t kv4_quantize8(const uint4& x, float (&r)[8]) {
+// Every lane runs the fast path; `rare` lanes are put right by kv4_quantize_rare, apart, so that the
+// fast paths of K and V lie in one basic block.
+struct Kv4Group {
+  float r[8];      // codes
+  uint32_t sm;     // s | m << 16
+  float lo, span;  // minimum, fp32 range
+  bool rare;
+};
+
+__device__ __forceinline__ Kv4Group kv4_quantize8(const uint4& x) {
+  Kv4Group g;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   __nv_bfloat162 h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
   const __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
   const __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+  const __nv_bfloat162 least = __hmin2(__hmin2(__habs2(h[0]), __habs2(h[1])), __hmin2(__habs2(h[2]), __habs2(h[3])));
   // (minimum, -maximum) in one word: a single minimum per shuffle serves both
-  __nv_bfloat162 e = __halves2bfloat162(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn)),
-                                        __hneg(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))));
+  const uint32_t mnw = *reinterpret_cast<const uint32_t*>(&mn), mxw = *reinterpret_cast<const uint32_t*>(&mx) ^ 0x80008000u;
+  const uint32_t lows = __byte_perm(mnw, mxw, 0x5410), highs = __byte_perm(mnw, mxw, 0x7632);
+  __nv_bfloat162 e = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&lows),
+                                 *reinterpret_cast<const __nv_bfloat162*>(&highs));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
     uint32_t u = *reinterpret_cast<uint32_t*>(&e);
     u = __shfl_xor_sync(0xffffffffu, u, o);
     e = __hmin2_nan(e, *reinterpret_cast<__nv_bfloat162*>(&u));
   }
-  const float lo = __low2float(e) + 0.0f;  // a zero minimum is stored as +0
-  const float span = -__high2float(e) - lo + 0.0f;
-  float q15 = span * (1.0f / 15.0f);
-  q15 = fmaf(fmaf(-15.0f, q15, span), 1.0f / 15.0f, q15);
-  // 2^-100 <= span: neither the remainder above nor rcp(s) below leaves the normal numbers
-  const bool plain = span >= 7.888609e-31f && span <= 3.4028234663852886e38f;
-  if (!plain) {
-    if (!(span <= 3.4028234663852886e38f)) {  // infinite or NaN values, or a range past fp32: the group is NaN
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-      return 0x7fc07fc0u;
-    }
-    q15 = __fdiv_rn(span, 15.0f);
-  }
-  const __nv_bfloat16 sb = __float2bfloat16_rn(q15);
-  const float s = __bfloat162float(sb);
+  const uint32_t ew = *reinterpret_cast<const uint32_t*>(&e);
+  g.lo = fma_bf16(ew, kBf16One, 0.0f);  // a zero minimum is stored as +0
+  g.span = -fma_bf16(ew >> 16, kBf16One, g.lo) + 0.0f;
+  float q15 = g.span * (1.0f / 15.0f);
+  q15 = fmaf(fmaf(-15.0f, q15, g.span), 1.0f / 15.0f, q15);
+  const uint32_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(q15));
+  const float s = __uint_as_float(sb << 16);
+  g.sm = sb | (__float_as_uint(g.lo) & 0xffff0000u);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to the nearest integer, ties to even
-    const float u0 = fma_bf16(w[i], kBf16One, -lo), u1 = fma_bf16(w[i] >> 16, kBf16One, -lo);
+    const float u0 = fma_bf16(w[i], kBf16One, -g.lo), u1 = fma_bf16(w[i] >> 16, kBf16One, -g.lo);
     float q0 = u0, q1 = u1, e0, e1;
     mul2(q0, q1, inv, inv);
     fma2(e0, e1, q0, q1, -s, -s, u0, u1);
     fma2(q0, q1, e0, e1, inv, inv, q0, q1);
     add2(q0, q1, kRound, kRound);
     add2(q0, q1, -kRound, -kRound);
-    r[2 * i] = q0;
-    r[2 * i + 1] = q1;
+    g.r[2 * i] = q0;
+    g.r[2 * i + 1] = q1;
   }
-  // the least magnitude, zeros included, settles it nearly always; else the least one that is not 0
-  // (magnitudes order like their bits, and less one a zero becomes the largest)
-  const __nv_bfloat162 least2 = __hmin2(__hmin2(__habs2(h[0]), __habs2(h[1])), __hmin2(__habs2(h[2]), __habs2(h[3])));
+  // 2^-100 <= span: neither q15's remainder nor rcp(s) leaves the normal numbers.  The least magnitude,
+  // zeros included, settles the precondition above nearly always.
   const float tiny = s * 0.000244140625f;  // 2^-12 s
-  bool fine = plain && (fabsf(lo) >= tiny || lo == 0.0f);
-  if (fminf(__low2float(least2), __high2float(least2)) < tiny) {
-    const uint32_t least = min_u16x2(min_u16x2(magnitude_less_one(w[0]), magnitude_less_one(w[1])),
-                                     min_u16x2(magnitude_less_one(w[2]), magnitude_less_one(w[3])));
-    fine = fine && min(least & 0xffffu, least >> 16) >= __float_as_uint(tiny) >> 16;
+  g.rare = !(g.span >= 7.888609e-31f && g.span <= 3.4028234663852886e38f &&
+             fminf(__low2float(least), __high2float(least)) >= tiny && fabsf(g.lo) >= tiny);
+  return g;
+}
+
+// The groups the fast path does not settle: non-finite, constant or tiny ranges, zeros and values
+// below 2^-12 s.
+__device__ __forceinline__ void kv4_quantize_rare(const uint4& x, Kv4Group& g) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if (!(g.span <= 3.4028234663852886e38f)) {  // infinite or NaN values, or a range past fp32: the group is NaN
+    g.sm = 0x7fc07fc0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g.r[i] = 0.0f;
+    return;
   }
-  if (span == 0.0f) {  // a constant group, or a token that is not there
+  if (g.span == 0.0f) {  // a constant group, or a token that is not there
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-  } else if (!fine) {
+    for (int i = 0; i < 8; ++i) g.r[i] = 0.0f;
+    return;
+  }
+  if (g.span < 7.888609e-31f)
+    g.sm = (g.sm & 0xffff0000u) | __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(g.span, 15.0f)));
+  const float s = bf16lo_to_f32(g.sm);
+  // magnitudes order like their bits; less one, a zero becomes the largest
+  const uint32_t least = min_u16x2(min_u16x2(magnitude_less_one(w[0]), magnitude_less_one(w[1])),
+                                   min_u16x2(magnitude_less_one(w[2]), magnitude_less_one(w[3])));
+  const uint32_t tiny = __float_as_uint(s * 0.000244140625f) >> 16;
+  if (g.span >= 7.888609e-31f && min(least & 0xffffu, least >> 16) >= tiny &&
+      ((__float_as_uint(g.lo) >> 16) & 0x7fffu) - 1u >= tiny)
+    return;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t wi = i == 0 ? w[0] : (i == 1 ? w[1] : (i == 2 ? w[2] : w[3]));
+    float c[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float xi = i % 2 == 0 ? bf16lo_to_f32(w[i / 2]) : bf16hi_to_f32(w[i / 2]);
-      const double q = ((double)xi - (double)lo) / (double)s;
-      r[i] = q >= 0.0 ? (float)fmin(rint(q), 15.0) : 0.0f;  // 0 / 0 (the scale underflowed): code 0
+    for (int k = 0; k < 2; ++k) {
+      const float xi = k == 0 ? bf16lo_to_f32(wi) : bf16hi_to_f32(wi);
+      const double q = ((double)xi - (double)g.lo) / (double)s;
+      c[k] = q >= 0.0 ? (float)fmin(rint(q), 15.0) : 0.0f;  // 0 / 0 (the scale underflowed): code 0
     }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (n == i) {
+        g.r[2 * n] = c[0];
+        g.r[2 * n + 1] = c[1];
+      }
   }
-  return (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
 // Values s c + m of 8 codes, rounded to bf16.
@@ -271,26 +304,23 @@ __global__ void __launch_bounds__(256) attn_kv4_append_kernel(const __grid_const
     uint32_t par = 0;  // the parameter word this lane stores: lanes 0.. of K's groups, lanes 4.. of V's
 #pragma unroll
     for (int y = 0; y < NG; ++y) {
-      float r[8];
-      uint32_t sm = kv4_quantize8(kx[y], r);
-      if (j == y) par = sm;
+      Kv4Group gk = kv4_quantize8(kx[y]), gv = kv4_quantize8(vx[y]);
+      if (gk.rare) kv4_quantize_rare(kx[y], gk);
+      if (gv.rare) kv4_quantize_rare(vx[y], gv);
+      if (j == y) par = gk.sm;
+      if (j == 4 + y) par = gv.sm;
       // even channels into the low half, odd ones into the high half; both sums are below 2^16,
       // and adding 2^23 leaves them in the low bits
-      float ev = r[6], od = r[7];
-      fma2(ev, od, ev, od, 16.0f, 16.0f, r[4], r[5]);
-      fma2(ev, od, ev, od, 16.0f, 16.0f, r[2], r[3]);
-      fma2(ev, od, ev, od, 16.0f, 16.0f, r[0], r[1]);
+      float ev = gk.r[6], od = gk.r[7];
+      fma2(ev, od, ev, od, 16.0f, 16.0f, gk.r[4], gk.r[5]);
+      fma2(ev, od, ev, od, 16.0f, 16.0f, gk.r[2], gk.r[3]);
+      fma2(ev, od, ev, od, 16.0f, 16.0f, gk.r[0], gk.r[1]);
       add2(ev, od, 8388608.0f, 8388608.0f);
       const uint32_t kw = __byte_perm(__float_as_uint(ev), __float_as_uint(od), 0x5410);
-      if (live) {
-        *reinterpret_cast<uint32_t*>(rec + kv4_k_code_off(y, ta, b0, b1, j)) = kw;
-        if (a.k_out != nullptr) *reinterpret_cast<uint4*>(a.k_out + out + 64 * y) = kv4_values8(r, sm);
-      }
-      sm = kv4_quantize8(vx[y], r);
-      if (j == 4 + y) par = sm;
-      float p0 = r[2], p1 = r[3], p4 = r[6], p5 = r[7];  // channels (0, 1) + 256 (2, 3) and (4, 5) + 256 (6, 7)
-      fma2(p0, p1, p0, p1, 256.0f, 256.0f, r[0], r[1]);
-      fma2(p4, p5, p4, p5, 256.0f, 256.0f, r[4], r[5]);
+      // channels (0, 1) + 256 (2, 3) and (4, 5) + 256 (6, 7)
+      float p0 = gv.r[2], p1 = gv.r[3], p4 = gv.r[6], p5 = gv.r[7];
+      fma2(p0, p1, p0, p1, 256.0f, 256.0f, gv.r[0], gv.r[1]);
+      fma2(p4, p5, p4, p5, 256.0f, 256.0f, gv.r[4], gv.r[5]);
       const uint32_t vw = __byte_perm(__float_as_uint(fmaf(p1, 16.0f, p0) + 8388608.0f),
                                       __float_as_uint(fmaf(p5, 16.0f, p4) + 8388608.0f), 0x5410);
       // a word holds both tokens of a pair: the even token's lane writes channels 0-3, the odd one's 4-7
@@ -303,7 +333,11 @@ __global__ void __launch_bounds__(256) attn_kv4_append_kernel(const __grid_const
         *reinterpret_cast<uint16_t*>(unit_v + 2 * b0) = (uint16_t)(vw & 0xffffu);
         *reinterpret_cast<uint16_t*>(unit_v + 4 + 2 * b0) = (uint16_t)(vw >> 16);
       }
-      if (live && a.v_out != nullptr) *reinterpret_cast<uint4*>(a.v_out + out + 64 * y) = kv4_values8(r, sm);
+      if (live) {
+        *reinterpret_cast<uint32_t*>(rec + kv4_k_code_off(y, ta, b0, b1, j)) = kw;
+        if (a.k_out != nullptr) *reinterpret_cast<uint4*>(a.k_out + out + 64 * y) = kv4_values8(gk.r, gk.sm);
+        if (a.v_out != nullptr) *reinterpret_cast<uint4*>(a.v_out + out + 64 * y) = kv4_values8(gv.r, gv.sm);
+      }
     }
     if (live && (j & 3) < NG)
       *reinterpret_cast<uint32_t*>(rec + kv4_param_off<NG>(j >> 2, ta, b0, b1) + 4 * (j & 3)) = par;
