@@ -55,6 +55,26 @@ attn_status launch_dependent(void (*k)(P...), dim3 grid, int threads, cudaStream
   return cudaLaunchKernelEx(&cfg, k, args...) == cudaSuccess ? launch_status() : ATTN_ERR_CUDA;
 }
 
+// Launches a grid of clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+attn_status launch_cluster(void (*k)(P...), dim3 grid, int cluster, int threads, size_t smem, cudaStream_t st,
+                           const A&... args) {
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...) == cudaSuccess ? launch_status() : ATTN_ERR_CUDA;
+}
+
 struct DecKv4Layout {
   size_t off_lse, off_o, total;
   long long warps;
@@ -77,7 +97,22 @@ DecKv4Layout kv4_layout(int S, int group, int d) {
 template <int D, int NT>
 attn_status launch_decode_kv4(const attn::DecKv4Args& a, cudaStream_t st, int slot) {
   using C = attn::DecKv4Cfg<D, NT>;
-  auto k = attn::attn_decode_kv4_split_kernel<D, NT>;
+  // Few short rows go out in one launch, a cluster a segment: 8.3 us instead of 12.3 for one row of 512
+  // tokens with 8 KV heads, 14.4 instead of 20.6 for 8 rows of 2048.  Not with fewer than 4 CTAs a
+  // segment (16 rows of 512: 14.5 against 14.4, with d = 256 20.5 against 20.5), and not for rows that
+  // could be longer than 1024 tokens a CTA (one row of 16384: 21.7 against 18.5), where the even cut over
+  // all SMs gains more than the launch.  The table's width bounds the lengths, which are on the device.
+  const long long segments = (long long)a.S * a.Hkv * a.n_hg, resident = (long long)sm_count() * C::CTAS_PER_SM;
+  int cluster = attn::kDecKv4MaxCluster;
+  while (cluster > attn::kDecKv4MinCluster && segments * cluster > resident) cluster /= 2;
+  if (segments * cluster <= resident && (long long)a.max_pages * a.page_size <= attn::kDecKv4ClusterTokens * cluster) {
+    attn::DecKv4Args b = a;
+    b.cluster = cluster;
+    auto kc = attn::attn_decode_kv4_split_kernel<D, NT, true>;
+    if (!ensure_smem(kc, C::SMEM, slot + 8)) return ATTN_ERR_CUDA;
+    return launch_cluster(kc, dim3((unsigned)(segments * cluster)), cluster, C::THREADS, C::SMEM, st, b);
+  }
+  auto k = attn::attn_decode_kv4_split_kernel<D, NT, false>;
   if (!ensure_smem(k, C::SMEM, slot)) return ATTN_ERR_CUDA;
   // no more CTAs than the longest possible rows can feed
   const double units = ((double)a.max_pages * a.page_size + attn::kDecKv4Unit - 1) / attn::kDecKv4Unit;
@@ -136,25 +171,6 @@ int copy_parts(size_t page_bytes) {
 bool small_table(int rows, int cols, int num_pages, double copies, const attn::PagePools& pp) {
   return rows <= attn::kSmallRows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages &&
          copies * pp.n * (double)pp.page_bytes <= (double)attn::kSmallBytes;
-}
-
-// Launches one cluster of kSmallCluster CTAs.
-template <typename... P, typename... A>
-attn_status launch_cluster(void (*k)(P...), int threads, size_t smem, cudaStream_t st, const A&... args) {
-  cudaLaunchAttribute attr;
-  std::memset(&attr, 0, sizeof(attr));
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = attn::kSmallCluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(attn::kSmallCluster);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...) == cudaSuccess ? launch_status() : ATTN_ERR_CUDA;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -272,6 +288,9 @@ attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int3
   if (q == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || (lse != nullptr && !aligned(lse, 4))) return ATTN_ERR_ALIGNMENT;
   if ((long long)num_seqs * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  // the units of all rows are counted in 32 bits
+  if ((double)num_seqs * (((double)max_pages_per_seq * page_size) / attn::kDecKv4Unit + 1.0) > 2147483647.0)
+    return ATTN_ERR_INVALID_ARG;
   const int group = Hq / Hkv;
   const DecKv4Layout L = kv4_layout(num_seqs, group, d);
   if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
@@ -369,7 +388,7 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   a.num_pages = num_pages;
   const int parts = copy_parts(page_bytes);
   if (small_table(new_rows, new_max_pages, num_pages, new_rows, pp))
-    return launch_cluster(attn::attn_pages_fork_small_kernel, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st,
+    return launch_cluster(attn::attn_pages_fork_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st,
                           a, pp);
   if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
   attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
@@ -421,7 +440,7 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   const int parts = copy_parts(page_bytes);
   // a page moves into a free one, so at most half of the pool moves
   if (small_table(num_seqs, max_pages_per_seq, num_pages, std::min((double)num_seqs * max_pages_per_seq, num_pages / 2.0), pp))
-    return launch_cluster(attn::attn_pages_compact_small_kernel, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4,
+    return launch_cluster(attn::attn_pages_compact_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4,
                           st, a, pp);
   if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
   attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);

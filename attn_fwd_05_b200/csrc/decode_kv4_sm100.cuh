@@ -45,6 +45,7 @@ struct DecKv4Args {
   float* part_o;               // workspace: [warps][2][8 NT][d]
   float* part_lse;             // workspace: [warps][2][8 NT], log2 units
   int S, Hq, Hkv, group, n_hg, page_size, lg_blocks, num_pages, max_pages;
+  int cluster;  // CTAs of a segment (the form for few short rows)
   float scale_log2;
 };
 
@@ -65,6 +66,9 @@ struct DecKv4Cfg {
 constexpr int kDecKv4Unit = 2 * kKv4Tok;  // tokens of a unit
 constexpr int kDecKv4MinUnits = 2;        // shortest range of a warp, in units
 constexpr int kDecKv4SegCost = 2;         // what starting and ending a segment costs, in units
+constexpr int kDecKv4MaxCluster = 8;      // most CTAs of a segment in the form for few short rows
+constexpr int kDecKv4MinCluster = 4;
+constexpr int kDecKv4ClusterTokens = 1024;  // longest row it takes, per CTA of the cluster
 
 // ------------------------------------------------------------------ fp16 and copy helpers
 
@@ -272,9 +276,73 @@ __device__ __forceinline__ void kv4_plan(const DecKv4Args& a, int4* first, long 
   __syncthreads();
 }
 
+// ------------------------------------------------------------------ joining partials
+
+template <int D, int W>
+struct Kv4JoinSmem {
+  float m[W], l[W], o[W][D];
+};
+
+// The block's W warps join np partials, at(k) the row of partial k, by their log-sum-exp, and write query
+// head `out` (a row of o and lse).  np = 0: an empty row.  The warps take every W-th partial.
+template <int D, int W, typename At>
+__device__ __forceinline__ void kv4_join(const DecKv4Args& a, int np, At at, size_t out, Kv4JoinSmem<D, W>& sh) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float M = -INFINITY;
+  for (int k = threadIdx.x; k < np; k += W * 32) M = fmaxf(M, a.part_lse[at(k)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) sh.m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) M = fmaxf(M, sh.m[w]);
+  const float u = M == -INFINITY ? 0.f : M;
+  float acc[PER], L = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int k = warp; k < np; k += W) {
+    const size_t pi = at(k);
+    const float x = a.part_lse[pi], e = ex2(x - u);
+    if (x == -INFINITY) continue;  // a warp without units: its O is not written
+    const float* po = a.part_o + pi * D + lane * PER;
+    L += e;
+#pragma unroll
+    for (int i = 0; i < PER; i += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(po + i);
+      acc[i] += e * v.x;
+      acc[i + 1] += e * v.y;
+    }
+  }
+  if (lane == 0) sh.l[warp] = L;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sh.o[warp][lane * PER + i] = acc[i];
+  __syncthreads();
+  if (warp == 0) {
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      L += sh.l[w];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += sh.o[w][lane * PER + i];
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    __nv_bfloat16* dst = a.o + out * D + lane * PER;
+#pragma unroll
+    for (int i = 0; i < PER; i += 2)
+      *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && a.lse != nullptr) a.lse[out] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
 // ------------------------------------------------------------------ split kernel
 
-template <int D, int NT>
+// CLUSTER: the form for few short rows, in one launch.  A cluster of a.cluster CTAs has one segment,
+// cut evenly over its warps, and joins their partials itself after a barrier.
+template <int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::CTAS_PER_SM)
     attn_decode_kv4_split_kernel(const __grid_constant__ DecKv4Args a) {
   using C = DecKv4Cfg<D, NT>;
@@ -284,12 +352,24 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
   __shared__ long long warp_sums[C::WARPS], begins[C::WARPS + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;  // row and column pair of the MMA fragments
-  kv4_plan<C::WARPS>(a, first, warp_sums, begins);
-  pdl_launch_dependents();
-  const int4 f = first[warp];
-  const int n = f.w;
-  if (n == 0) return;
   const int wid = blockIdx.x * C::WARPS + warp;
+  int4 f;
+  if constexpr (CLUSTER) {
+    const int k = blockIdx.x / a.cluster, C_ = a.Hkv * a.n_hg;
+    f = make_int4(k / C_, k % C_, 0, 0);
+    const int len = __ldg(&a.seq_lens[f.x]);
+    if ((len < 0 || len > a.max_pages * a.page_size) && lane == 0) latch_status(ATTN_ERR_INVALID_ARG);
+    const int nt = kv4_units(a, f.x), warps = a.cluster * C::WARPS, per = (nt + warps - 1) / warps;
+    f.z = min(nt, wid % warps * per);
+    f.w = min(per, nt - f.z);
+    if (f.w == 0 && lane < C::ROWS) a.part_lse[(size_t)2 * wid * C::ROWS + lane] = -INFINITY;
+  } else {
+    kv4_plan<C::WARPS>(a, first, warp_sums, begins);
+    pdl_launch_dependents();
+    f = first[warp];
+    if (f.w == 0) return;
+  }
+  const int n = f.w;
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::UNIT);
 
   // ---- fetch side: lane l keeps the record number of tile l % 2 of unit l / 2 of the current
@@ -297,7 +377,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
   // batch, whose table loads are then in flight long before they are needed
   Kv4Cursor fc{f.x, f.y, f.z, 0};
   fc.nt = kv4_units(a, fc.s);
-  fc.forward(a, lane >> 1);
+  if (n > 0) fc.forward(a, lane >> 1);
   auto record_of = [&](int unit) -> int {
     if (unit >= n || fc.s >= a.S) return -1;
     const int tile = 2 * fc.t + (lane & 1);
@@ -404,7 +484,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
 #pragma unroll
     for (int y = 0; y < NG; ++y) unit[y] = pow2i(100);
   };
-  begin();
+  if (n > 0) begin();
 
   uint32_t out = ring;
   for (int i = 0; i < n; ++i) {
@@ -593,9 +673,9 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
     const bool end = left <= kDecKv4Unit;
     left -= kDecKv4Unit;
     if (end || i == n - 1) {
-      const bool whole = end && !cut;
+      const bool whole = !CLUSTER && end && !cut;
       const int nrows = rows_of(cc), hq0 = head_of(cc);
-      const size_t prow = (size_t)(2 * wid + (cut ? 0 : 1)) * C::ROWS;
+      const size_t prow = (size_t)(2 * wid + (CLUSTER || cut ? 0 : 1)) * C::ROWS;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -648,83 +728,45 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
     }
   }
   cp_async_wait<0>();
+  if constexpr (CLUSTER) {
+    __shared__ Kv4JoinSmem<D, C::WARPS> sh;
+    cluster_barrier();
+    const int rank = blockIdx.x % a.cluster, nrows = rows_of(f.y);
+    const int w0 = blockIdx.x / a.cluster * (a.cluster * C::WARPS);
+    for (int row = rank; row < nrows; row += a.cluster) {
+      auto at = [&](int k) -> size_t { return (size_t)2 * (w0 + k) * C::ROWS + row; };
+      kv4_join<D, C::WARPS>(a, kv4_units(a, f.x) > 0 ? a.cluster * C::WARPS : 0, at,
+                            (size_t)f.x * a.Hq + head_of(f.y) + row, sh);
+      __syncthreads();
+    }
+  }
 }
 
 // ------------------------------------------------------------------ merge kernel
 
 // One CTA per (sequence, query head): joins the partials of a segment that more than one warp's
-// range shares; writes the rows of empty sequences.  Its W warps take every W-th partial.  Few
-// rows have many partials each (one per warp of the split kernel that had a part of the row) and
-// get 16 warps; many rows have few each and get 4.  Measured on two rows of 131071 tokens (146
-// partials a head): 21 us with 4 warps, 9 us with 16.
+// range shares; writes the rows of empty sequences.  Few rows have many partials each (one per warp
+// of the split kernel that had a part of the row) and get 16 warps; many rows have few each and
+// get 4.  Measured on two rows of 131071 tokens (110 partials a head): 21 us with 4 warps, 9 us with 16.
 template <int D, int NT, int W>
 __global__ void __launch_bounds__(W * 32) attn_decode_kv4_merge_kernel(const __grid_constant__ DecKv4Args a) {
   using C = DecKv4Cfg<D, NT>;
-  constexpr int PER = D / 32;
-  __shared__ float sh_m[W], sh_l[W], sh_o[W][D];
+  __shared__ Kv4JoinSmem<D, W> sh;
   const int s = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   const long long p0 = a.unit_prefix[s], p1 = a.unit_prefix[s + 1], per = a.unit_prefix[a.S + 1];
   const int nt = max(0, (int)(p1 - p0) - kDecKv4SegCost);
-  float acc[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  float M = -INFINITY, L = 0.f;
-  if (nt > 0) {
-    const int in_kv = h % a.group;
-    const int c = (h / a.group) * a.n_hg + in_kv / C::ROWS;
-    const int row = in_kv % C::ROWS;
-    // the costs of the segment's first unit and of the one after its last
-    const long long f0 = p0 * (a.Hkv * a.n_hg) + (long long)c * (nt + kDecKv4SegCost) + kDecKv4SegCost, f1 = f0 + nt;
-    const long long w0 = f0 / per;
-    const int np = (int)((f1 - 1) / per - w0) + 1;
-    if (np == 1) return;  // finished by the warp that had all of it
-    // the first warp's partial is the one it ended its range with (slot 1), the others' began before them
-    auto at = [&](int k) -> size_t { return (size_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row; };
-    for (int k = threadIdx.x; k < np; k += W * 32) M = fmaxf(M, a.part_lse[at(k)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) sh_m[warp] = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, sh_m[w]);
-    const float u = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-    for (int k = warp; k < np; k += W) {
-      const size_t pi = at(k);
-      const float e = ex2(a.part_lse[pi] - u);
-      L += e;
-      const float* po = a.part_o + pi * D + lane * PER;
-#pragma unroll
-      for (int i = 0; i < PER; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(po + i);
-        acc[i] = fmaf(e, v.x, acc[i]);
-        acc[i + 1] = fmaf(e, v.y, acc[i + 1]);
-      }
-    }
-    if (lane == 0) sh_l[warp] = L;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) sh_o[warp][lane * PER + i] = acc[i];
-    __syncthreads();
-    L = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      L += sh_l[w];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += sh_o[w][lane * PER + i];
-    }
-  }
-  if (warp != 0) return;
-  const float inv = L != 0.f ? 1.f / L : 0.f;
-  __nv_bfloat16* dst = a.o + ((size_t)s * a.Hq + h) * D + lane * PER;
-#pragma unroll
-  for (int i = 0; i < PER; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[(size_t)s * a.Hq + h] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  const int in_kv = h % a.group;
+  const int c = (h / a.group) * a.n_hg + in_kv / C::ROWS;
+  const int row = in_kv % C::ROWS;
+  // the costs of the segment's first unit and of the one after its last
+  const long long f0 = p0 * (a.Hkv * a.n_hg) + (long long)c * (nt + kDecKv4SegCost) + kDecKv4SegCost, f1 = f0 + nt;
+  const long long w0 = f0 / per;
+  const int np = nt > 0 ? (int)((f1 - 1) / per - w0) + 1 : 0;
+  if (np == 1) return;  // finished by the warp that had all of it
+  // the first warp's partial is the one it ended its range with (slot 1), the others' began before them
+  auto at = [&](int k) -> size_t { return (size_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row; };
+  kv4_join<D, W>(a, np, at, (size_t)s * a.Hq + h, sh);
 }
 
 }  // namespace attn

@@ -370,8 +370,10 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  *                aligned, overwritten; two calls in flight at once need two workspaces
  * Other arguments, empty sequences and bad pages as in attn_decode_paged.  A sequence length outside
  * [0, max_pages_per_seq * page_size] counts as 0 and latches ATTN_ERR_INVALID_ARG.  What a page
- * holds past its sequence's end is never used.  Two kernels, whose result does not depend on the
- * order in which the GPU runs them.
+ * holds past its sequence's end is never used.  num_seqs * (max_pages_per_seq * page_size / 32 + 1) must
+ * be below 2^31.  One kernel for few sequences of a narrow table, else two; the result does not depend
+ * on the order in which the GPU runs their blocks.  How a row's sums are split depends on the other
+ * rows' lengths and on the table's width, so the last bits of a row may differ between batches.
  */
 attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int32_t* block_table,
                                   const int32_t* seq_lens, int page_size, void* o, float* lse, int num_seqs,

@@ -101,6 +101,7 @@ def dec(lib, q=FAKE, pool=FAKE, bt=FAKE, sl=FAKE, ps=16, o=FAKE, lse=None, S=4, 
     (dict(o=None), INVALID), (dict(bt=None), INVALID), (dict(sl=None), INVALID), (dict(pool=None), INVALID),
     (dict(q=FAKE + 8), ALIGN), (dict(o=FAKE + 4), ALIGN), (dict(pool=FAKE + 8), ALIGN), (dict(lse=FAKE + 2), ALIGN),
     (dict(ws=FAKE + 16), ALIGN), (dict(ws=None), WORKSPACE), (dict(wsb=100), WORKSPACE),
+    (dict(S=100000, maxp=1 << 20), INVALID), (dict(S=1 << 14, maxp=1 << 18), INVALID),  # 2^31 units of 32 tokens
 ])
 def test_decode_rejects_bad_arguments(lib, kw, code):
     assert dec(lib, **kw) == code

@@ -126,6 +126,12 @@ def check_decode(o, lse, q, pool, table, lens, page_size, scale):
             assert le <= e + n * 2.0 ** -24 + 2.0 ** -22 * abs(ref_l[i, h]) + 2.0 ** -21, f"row {i} head {h}: lse off by {le:.2e}"
 
 
+def widen(table, page_size, tokens=20000):
+    """The table with columns for rows of up to `tokens`: the host then has to expect long rows."""
+    more = np.full((table.shape[0], -(-tokens // page_size)), -1, dtype=np.int32)
+    return np.ascontiguousarray(np.concatenate([table, more], axis=1))
+
+
 CASES = [
     # lens, Hq, Hkv, d, page_size
     ([1], 1, 1, 64, 16),
@@ -139,14 +145,20 @@ CASES = [
     ([300, 40], 64, 1, 64, 16),                     # 64 per KV head
     ([2500], 3, 1, 128, 64),                        # odd group
     ([310, 4000], 27, 3, 128, 16),                  # odd head counts, group 9
+    # around 64 segments: smaller clusters
+    ([1, 2, 31, 0, 32, 33, 1000, 127, 128, 129, 4096], 16, 8, 128, 16),
+    ([700, 64, 3, 2047, 0, 500, 12, 90], 18, 9, 256, 32),
+    ([333, 100, 1], 16 * 18, 16, 64, 64),           # 18 per KV head: 96 segments
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens,Hq,Hkv,d,ps", CASES)
-def test_decode_matches_oracle(lens, Hq, Hkv, d, ps, cuda_device):
+def test_decode_matches_oracle(lens, Hq, Hkv, d, ps, wide, cuda_device):
     rng = np.random.default_rng(Hq * d + len(lens))
     table, num_pages = layout(rng, lens, ps)
     pool = poison_unused(random_pool(rng, num_pages, Hkv, ps, d), table, lens, ps, d)
+    table = widen(table, ps) if wide else table
     q = bf16(rng, (len(lens), Hq, d))
     scale = 1.0 / math.sqrt(d)
     o, lse, status = run_decode(q, pool, table, lens, ps, scale)
@@ -166,11 +178,13 @@ def test_decode_of_many_rows(cuda_device):
     check_decode(o, lse, q, pool, table, lens, 16, 0.125)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kind", ["peaked", "rising", "growing_v", "tiny_v", "huge_v", "flat", "large_q", "small_q"])
-def test_decode_value_ranges(kind, cuda_device):
+def test_decode_value_ranges(kind, wide, cuda_device):
     rng = np.random.default_rng(17)
     d, ps, lens = 128, 16, [1111, 600]
     table, num_pages = layout(rng, lens, ps)
+    table = widen(table, ps) if wide else table
     pool = random_pool(rng, num_pages, 2, ps, d)
     q = bf16(rng, (2, 8, d))
     scale = 1.0 / math.sqrt(d)
@@ -208,10 +222,12 @@ def test_decode_value_ranges(kind, cuda_device):
     check_decode(o, lse, q, pool, table, lens, ps, scale)
 
 
-def test_decode_is_repeatable_and_placement_free(cuda_device):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_is_repeatable_and_placement_free(wide, cuda_device):
     rng = np.random.default_rng(8)
     lens = [700, 33, 2900]
     table, num_pages = layout(rng, lens, 32)
+    table = widen(table, 32) if wide else table
     pool = random_pool(rng, num_pages, 2, 32, 128)
     q = bf16(rng, (3, 8, 128))
     o1, l1, _ = run_decode(q, pool, table, lens, 32, 0.09)
@@ -226,10 +242,12 @@ def test_decode_is_repeatable_and_placement_free(cuda_device):
         assert torch.equal(o1, o) and torch.equal(l1, lse)
 
 
-def test_decode_nan_groups_stay_in_their_rows(cuda_device):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_nan_groups_stay_in_their_rows(wide, cuda_device):
     rng = np.random.default_rng(9)
     lens, d = [200, 200], 128
     table, num_pages = layout(rng, lens, 16)
+    table = widen(table, 16) if wide else table
     pool = random_pool(rng, num_pages, 1, 16, d)
     rec = pool.reshape(num_pages, 1, 1, -1)
     # V group 1 of token 37 of row 0 is NaN; K of token 5 of row 1 too
@@ -246,10 +264,12 @@ def test_decode_nan_groups_stay_in_their_rows(cuda_device):
     assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all() and torch.isfinite(lse[0]).all()
 
 
-def test_decode_bad_pages_and_lengths_are_reported(cuda_device):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_bad_pages_and_lengths_are_reported(wide, cuda_device):
     rng = np.random.default_rng(10)
     lens = [100, 50, 64]
     table, num_pages = layout(rng, lens, 16)
+    table = widen(table, 16) if wide else table
     pool = random_pool(rng, num_pages, 2, 16, 128)
     q = bf16(rng, (3, 8, 128))
     t = table.copy()
@@ -565,10 +585,12 @@ def test_serving_run_in_a_graph_and_on_another_stream(cuda_device):
     del g
 
 
-def test_two_decodes_in_flight(cuda_device):
+@pytest.mark.parametrize("wide", [False, True])
+def test_two_decodes_in_flight(wide, cuda_device):
     rng = np.random.default_rng(43)
     lens = [900, 1700]
     table, num_pages = layout(rng, lens, 16)
+    table = widen(table, 16) if wide else table
     pool = random_pool(rng, num_pages, 2, 16, 128)
     q = [bf16(rng, (2, 8, 128)) for _ in range(2)]
     want = [run_decode(x, pool, table, lens, 16, 0.09)[:2] for x in q]
@@ -619,11 +641,13 @@ def test_binding_refusals(cuda_device):
     assert ab.attn_get_device_status() == 0
 
 
-def test_decode_does_not_depend_on_what_shared_memory_held(cuda_device):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_does_not_depend_on_what_shared_memory_held(wide, cuda_device):
     # rows that end inside a unit of two records, after calls on other data left their records behind
     rng = np.random.default_rng(44)
     lens = [5, 16, 17, 31, 33, 200, 1000]
     table, num_pages = layout(rng, lens, 16)
+    table = widen(table, 16) if wide else table
     pool = random_pool(rng, num_pages, 2, 16, 128)
     q = bf16(rng, (len(lens), 8, 128))
     o0, l0, _ = run_decode(q, pool, table, lens, 16, 0.09)
