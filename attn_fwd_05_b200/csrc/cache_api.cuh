@@ -27,13 +27,13 @@ attn_status kv4_check(const void* pool, const int32_t* table, const int32_t* seq
 
 template <int NG>
 attn_status launch_append(const attn::Kv4AppendArgs& a, unsigned grid, cudaStream_t st) {
-  attn::attn_kv4_append_kernel<NG><<<grid, 256, 0, st>>>(a);
+  attn::attn_kv4_append_kernel<NG><<<grid, attn::kKv4AppendThreads, 0, st>>>(a);
   return launch_status();
 }
 
 template <int NG>
 attn_status launch_gather(const attn::Kv4GatherArgs& a, unsigned grid, cudaStream_t st) {
-  attn::attn_kv4_gather_kernel<NG><<<grid, attn::Kv4GatherCfg<NG>::WARPS * 32, 0, st>>>(a);
+  attn::attn_kv4_gather_kernel<NG><<<grid, attn::kKv4GatherWarps * 32, 0, st>>>(a);
   return launch_status();
 }
 
@@ -166,11 +166,13 @@ int copy_parts(size_t page_bytes) {
   return (int)std::max<size_t>(1, std::min<size_t>(32, page_bytes / 16384));
 }
 
-// One launch of one cluster: cheaper than a clearing and two kernels while one CTA plans the entries
-// in a few rounds and 8 CTAs copy what there can be to copy in a few microseconds.
-bool small_table(int rows, int cols, int num_pages, double copies, const attn::PagePools& pp) {
+// One launch of one cluster is cheaper than a clearing and two kernels (8 rows of 64 pages: fork 7.1 us
+// instead of 9.3, compact 7.6 instead of 10.3) while one CTA plans the entries in a round or two (16 x
+// 128: 10.1 and 11.5 us against 11.9 and 12.3; 32 x 128: 14.4 and 16.9 against 13.7 and 14.3) and 8 CTAs
+// copy at most `bytes` (8 forked rows of 128 KB pages: 10.1 us against 12.3; 64 of 32 KB: 16.0 against 12.3).
+bool small_table(int rows, int cols, int num_pages, double copies, const attn::PagePools& pp, long long bytes) {
   return rows <= attn::kSmallRows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages &&
-         copies * pp.n * (double)pp.page_bytes <= (double)attn::kSmallBytes;
+         copies * pp.n * (double)pp.page_bytes <= (double)bytes;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -201,6 +203,13 @@ attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int6
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_new, 4) || (k_out && !aligned(k_out, 16)) ||
       (v_out && !aligned(v_out, 16)) || k_stride % 8 != 0 || v_stride % 8 != 0)
     return ATTN_ERR_ALIGNMENT;
+  // written rows may be the rows read (each lane writes what it has read), not others of them
+  const size_t row = (size_t)Hkv * d * 2, in_k = (size_t)(num_new - 1) * k_stride * 2 + row,
+               in_v = (size_t)(num_new - 1) * v_stride * 2 + row, out = (size_t)num_new * row;
+  if ((k_out && (overlap(k_out, out, v, in_v) || (overlap(k_out, out, k, in_k) && (k_out != k || out != in_k)))) ||
+      (v_out && (overlap(v_out, out, k, in_k) || (overlap(v_out, out, v, in_v) && (v_out != v || out != in_v)))) ||
+      (k_out && v_out && overlap(k_out, out, v_out, out)))
+    return ATTN_ERR_INVALID_ARG;
   attn::Kv4AppendArgs a;
   std::memset(&a, 0, sizeof(a));
   a.k = static_cast<const __nv_bfloat16*>(k);
@@ -222,7 +231,8 @@ attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int6
   // as many heads a warp as leave some 48 warps to every SM
   const long long quads = (long long)(num_new >> 2) + 2ll * num_seqs;
   a.heads = (int)std::max(1ll, std::min<long long>(Hkv, quads * Hkv / (48ll * sm_count())));
-  const long long grid = (quads * ((Hkv + a.heads - 1) / a.heads) + 7) / 8;
+  const int warps = attn::kKv4AppendThreads / 32;
+  const long long grid = (quads * ((Hkv + a.heads - 1) / a.heads) + warps - 1) / warps;
   if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d) {
@@ -258,10 +268,8 @@ attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, con
   // N may be larger than any row: records past a row's capacity have no work
   const long long nrec = ((long long)N + 15) / 16;
   const long long units = nrec * num_seqs;
-  if (units > 0x7fffffffLL * 4 / Hkv) return ATTN_ERR_INVALID_ARG;
-  a.heads = (int)std::max(1ll, std::min<long long>(Hkv, units * Hkv / (48ll * sm_count())));
-  const int warps = d == 256 ? 4 : 8;
-  const unsigned grid = (unsigned)((units * ((Hkv + a.heads - 1) / a.heads) + warps - 1) / warps);
+  if (units > 0x7fffffffLL * attn::kKv4GatherWarps / Hkv) return ATTN_ERR_INVALID_ARG;
+  const unsigned grid = (unsigned)((units * Hkv + attn::kKv4GatherWarps - 1) / attn::kKv4GatherWarps);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d) {
     case 64: return launch_gather<1>(a, grid, st);
@@ -387,9 +395,9 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   a.page_size = page_size;
   a.num_pages = num_pages;
   const int parts = copy_parts(page_bytes);
-  if (small_table(new_rows, new_max_pages, num_pages, new_rows, pp))
-    return launch_cluster(attn::attn_pages_fork_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st,
-                          a, pp);
+  if (small_table(new_rows, new_max_pages, num_pages, new_rows, pp, attn::kSmallForkBytes))
+    return launch_cluster(attn::attn_pages_fork_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster,
+                          attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st, a, pp);
   if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
   attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
@@ -439,9 +447,10 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   a.num_pages = num_pages;
   const int parts = copy_parts(page_bytes);
   // a page moves into a free one, so at most half of the pool moves
-  if (small_table(num_seqs, max_pages_per_seq, num_pages, std::min((double)num_seqs * max_pages_per_seq, num_pages / 2.0), pp))
-    return launch_cluster(attn::attn_pages_compact_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster, attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4,
-                          st, a, pp);
+  const double moves = std::min((double)num_seqs * max_pages_per_seq, num_pages / 2.0);
+  if (small_table(num_seqs, max_pages_per_seq, num_pages, moves, pp, attn::kSmallCompactBytes))
+    return launch_cluster(attn::attn_pages_compact_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster,
+                          attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4, st, a, pp);
   if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
   attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;

@@ -55,6 +55,7 @@ struct Kv4AppendArgs {
   int S, T, Hkv, page_size, num_pages, max_pages;
   int heads;  // KV heads a warp takes in turn
 };
+constexpr int kKv4AppendThreads = 128;
 
 // a b + c with bf16 a and b (16-bit halves of a word, say) and fp32 c: one FMA, where widening
 // a half first would cost an instruction of the half-rate integer pipe.
@@ -238,12 +239,16 @@ __device__ __forceinline__ int kv4_find_seq(const int32_t* cu, int S, long long 
 // One warp per aligned quad of positions and `heads` KV heads: lane = 8 (token of the quad) +
 // (8-channel chunk).  The reads are bf16 rows of 128 bytes a group; the quad's K codes and V codes
 // are one 128-byte line a group each.  A call is bound by HBM (2 d bytes read and 9 d / 16
-// written per token, head and tensor) once every SM has enough loads in flight: a warp therefore
-// takes several heads where there are warps to spare, since its chain of dependent loads (sequence,
-// position, page) then serves all of them, and fetches the next head's rows while it works
-// on one.  108K tokens, 8 heads, d = 128, with the values written back: @@.
+// written per token, head and tensor, and 2 d more where the values are written back) once every SM
+// has enough loads in flight: a warp therefore takes several heads where there are warps to spare, since
+// its chain of dependent loads (sequence, position, page) then serves all of them (108K tokens, 8
+// heads, d = 128: 359 us with one head a warp, 272 with 2, 229 with 4, 216 with 8; a decode step of 64
+// tokens 6.2 us with one and 14.4 with 8), and fetches the next head's rows while it works on one
+// (without: 254).  Small blocks and a few spilled words leave room for 20 warps an SM instead of
+// 16: 199 us, 5.6 TB/s (24 warps with 108 bytes spilled: 245); d = 256: 413 us instead of 505.
 template <int NG>
-__global__ void __launch_bounds__(256) attn_kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kKv4AppendThreads, NG == 1 ? 6 : (NG == 2 ? 5 : 3))
+    attn_kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
   constexpr int D = NG * kKv4Group;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(256) attn_kv4_append_kernel(const __grid_const
   }
   const int start = len - n;
   const long long quad = (start >> 2) + (q - qs);  // quad of positions
-  if (q < qs || 4 * quad >= len) return;
+  if (n == 0 || q < qs || 4 * quad >= len) return;
   const int i = lane >> 3, j = lane & 7;
   const int pos = (int)(4 * quad) + i;
   const bool live = pos >= start && pos < len;
@@ -353,7 +358,6 @@ struct Kv4GatherArgs {
   __nv_bfloat16* k;  // [S, Hkv, N, d]
   __nv_bfloat16* v;
   int S, Hkv, N, page_size, num_pages, max_pages;
-  int heads;  // KV heads a warp takes in turn
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -376,28 +380,23 @@ __device__ __forceinline__ void kv4_fetch_record(uint32_t dst, const uint8_t* sr
   }
 }
 
-template <int NG>
-struct Kv4GatherCfg {
-  static constexpr int WARPS = NG == 4 ? 4 : 8;
-  static constexpr int STAGES = 2;
-};
+constexpr int kKv4GatherWarps = 8;
 
-// One warp per 16 positions of a sequence and `heads` KV heads.  The work is a copy (9 d / 8 bytes
-// in and 4 d out per token and head), so what counts is loads in flight: records come in whole by
-// 16-byte asynchronous copies, the next head's while one is written out, and the lanes take their
-// codes from shared memory (lane = 8 (token of a quad) + (8-channel chunk), as in the append).
+// One warp per record: 16 positions of a sequence and a KV head.  The work is a copy (9 d / 8 bytes in
+// and 4 d out per token and head), so what counts is loads in flight: a record comes in whole by
+// 16-byte asynchronous copies, and the lanes take their codes from shared memory (lane = 8 (token of a
+// quad) + (8-channel chunk), as in the append).  8 contexts of 15 to 16.4 thousand tokens, 8 heads, d =
+// 128: 112 us, 5.9 TB/s; with all heads in turn in one warp, the next record on its way, 117 us.
 template <int NG>
-__global__ void __launch_bounds__(Kv4GatherCfg<NG>::WARPS * 32)
+__global__ void __launch_bounds__(kKv4GatherWarps * 32)
     attn_kv4_gather_kernel(const __grid_constant__ Kv4GatherArgs a) {
   constexpr int D = NG * kKv4Group, REC = kv4_record_bytes(D);
-  using C = Kv4GatherCfg<NG>;
-  __shared__ __align__(128) uint8_t stage[C::WARPS][C::STAGES][REC];
+  __shared__ __align__(128) uint8_t stage[kKv4GatherWarps][REC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = (long long)blockIdx.x * C::WARPS + warp;
+  const long long unit = (long long)blockIdx.x * kKv4GatherWarps + warp;
   const int nrec = (a.N + kKv4Tok - 1) / kKv4Tok;
-  const int parts = (a.Hkv + a.heads - 1) / a.heads;
-  const int h0 = (int)(unit % parts) * a.heads, h1 = min(a.Hkv, h0 + a.heads);
-  const long long sr = unit / parts;
+  const int h = (int)(unit % a.Hkv);
+  const long long sr = unit / a.Hkv;
   const int r0 = (int)(sr % nrec);
   const long long sq = sr / nrec;
   if (sq >= a.S) return;
@@ -415,46 +414,36 @@ __global__ void __launch_bounds__(Kv4GatherCfg<NG>::WARPS * 32)
     latch_status(ATTN_ERR_BAD_PAGE);
     return;
   }
-  const int blocks = a.page_size / kKv4Tok;
-  const size_t head_bytes = (size_t)blocks * REC;
-  const uint8_t* rec = a.pool + ((size_t)page * a.Hkv + h0) * head_bytes + (size_t)((p0 % a.page_size) / kKv4Tok) * REC;
-  const int i = lane >> 3, j = lane & 7, b0 = i & 1, b1 = i >> 1;
-  kv4_fetch_record<REC>(smem_u32(stage[warp][0]), rec, lane);
+  const size_t at = ((size_t)page * a.Hkv + h) * (a.page_size / kKv4Tok) + (p0 % a.page_size) / kKv4Tok;
+  const uint8_t* st = stage[warp];
+  kv4_fetch_record<REC>(smem_u32(st), a.pool + at * REC, lane);
   cp_async_commit();
-#pragma unroll 1
-  for (int h = h0; h < h1; ++h) {
-    rec += head_bytes;
-    if (h + 1 < h1) kv4_fetch_record<REC>(smem_u32(stage[warp][(h + 1 - h0) & 1]), rec, lane);
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncwarp();
-    const uint8_t* st = stage[warp][(h - h0) & 1];
-    const size_t row0 = ((size_t)s * a.Hkv + h) * a.N + p0 + i;
-#pragma unroll
-    for (int ta = 0; ta < 4; ++ta) {
-      if (p0 + 4 * ta + i >= len) break;
-      const size_t out = (row0 + 4 * ta) * D + 8 * j;
-#pragma unroll
-      for (int y = 0; y < NG; ++y) {
-        const uint32_t ksm = *reinterpret_cast<const uint32_t*>(st + kv4_param_off<NG>(0, ta, b0, b1) + 4 * y);
-        const uint32_t vsm = *reinterpret_cast<const uint32_t*>(st + kv4_param_off<NG>(1, ta, b0, b1) + 4 * y);
-        const uint32_t kw = *reinterpret_cast<const uint32_t*>(st + kv4_k_code_off(y, ta, b0, b1, j));
-        const uint2 vu = *reinterpret_cast<const uint2*>(st + kv4_v_unit_off<NG>(y, ta, j) + 8 * b1);
-        float lo[4], hi[4];
-        kv4_code_values(kw, ksm, lo, hi);  // channels 2i and 2i + 1
-        __stcs(reinterpret_cast<uint4*>(a.k + out + 64 * y),
-               make_uint4(pack_bf16x2(lo[0], hi[0]), pack_bf16x2(lo[1], hi[1]), pack_bf16x2(lo[2], hi[2]),
-                          pack_bf16x2(lo[3], hi[3])));
-        // this token's halves of the two words: channels i and 4 + i
-        kv4_code_values(__byte_perm(vu.x, vu.y, b0 == 0 ? 0x5410 : 0x7632), vsm, lo, hi);
-        __stcs(reinterpret_cast<uint4*>(a.v + out + 64 * y),
-               make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
-                          pack_bf16x2(hi[2], hi[3])));
-      }
-    }
-    __syncwarp();  // the stage is refilled two heads later
-  }
   cp_async_wait<0>();
+  __syncwarp();
+  const int i = lane >> 3, j = lane & 7, b0 = i & 1, b1 = i >> 1;
+  const size_t row0 = ((size_t)s * a.Hkv + h) * a.N + p0 + i;
+#pragma unroll
+  for (int ta = 0; ta < 4; ++ta) {
+    if (p0 + 4 * ta + i >= len) break;
+    const size_t out = (row0 + 4 * ta) * D + 8 * j;
+#pragma unroll
+    for (int y = 0; y < NG; ++y) {
+      const uint32_t ksm = *reinterpret_cast<const uint32_t*>(st + kv4_param_off<NG>(0, ta, b0, b1) + 4 * y);
+      const uint32_t vsm = *reinterpret_cast<const uint32_t*>(st + kv4_param_off<NG>(1, ta, b0, b1) + 4 * y);
+      const uint32_t kw = *reinterpret_cast<const uint32_t*>(st + kv4_k_code_off(y, ta, b0, b1, j));
+      const uint2 vu = *reinterpret_cast<const uint2*>(st + kv4_v_unit_off<NG>(y, ta, j) + 8 * b1);
+      float lo[4], hi[4];
+      kv4_code_values(kw, ksm, lo, hi);  // channels 2i and 2i + 1
+      __stcs(reinterpret_cast<uint4*>(a.k + out + 64 * y),
+             make_uint4(pack_bf16x2(lo[0], hi[0]), pack_bf16x2(lo[1], hi[1]), pack_bf16x2(lo[2], hi[2]),
+                        pack_bf16x2(lo[3], hi[3])));
+      // this token's halves of the two words: channels i and 4 + i
+      kv4_code_values(__byte_perm(vu.x, vu.y, b0 == 0 ? 0x5410 : 0x7632), vsm, lo, hi);
+      __stcs(reinterpret_cast<uint4*>(a.v + out + 64 * y),
+             make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                        pack_bf16x2(hi[2], hi[3])));
+    }
+  }
 }
 
 }  // namespace attn

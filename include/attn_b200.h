@@ -296,7 +296,8 @@ size_t attn_decode_paged_noalloc_max_scratch(void);
  *     m = min (a zero as +0),  s = bf16((max - min) / 15) with the subtraction and the division
  *     in fp32, c = the integer nearest to (x - m) / s, ties to even, at most 15.
  * The quotient that decides c is taken exactly, not from a rounded fp32 division.  A group with an
- * infinite or NaN value, or whose range overflows fp32, is stored as NaN (s = m = NaN).
+ * infinite or NaN value, or whose range overflows fp32, is stored as NaN (s = m = NaN).  Pools filled
+ * by other means must keep s at +0 or above (or NaN).
  *
  * kv_pool: uint8 [num_pages, Hkv, page_size / 16, record], 16-byte aligned.  A record holds K and V
  * of 16 consecutive tokens of one KV head in 1152 * NG bytes, NG = d / 64.  With token (within the
@@ -326,7 +327,8 @@ size_t attn_kv4_page_bytes(int Hkv, int page_size, int d);
  *                cu_new[s + 1] - 1 of k and v are the last tokens of sequence s
  *   k_out, v_out device, bf16 [num_new, Hkv, d] (dense, 16-byte aligned) or NULL: written with the
  *                values the cache now stands for, rounded to bf16, so that a prompt's own attention can
- *                see exactly what later decode steps will see
+ *                see exactly what later decode steps will see.  k_out may be a dense k itself and v_out a
+ *                dense v; any other overlap of an output with k, v or the other output is refused
  * A slot must not be written by two tokens of one call (pages shared between rows are for reading:
  * see attn_pages_fork).  A table entry in use outside [0, num_pages) is skipped and latches
  * ATTN_ERR_BAD_PAGE; a sequence whose seq_lens or cu_new entries are out of range is skipped and
@@ -364,7 +366,7 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  * cached values x = s * c + m.  The codes enter the matrix products exactly; scores, running maxima
  * and sums are fp32, and the probabilities are rounded to 11 bits before P V.
  *
- *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned
+ *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned, not overlapping
  *   lse          device, fp32 [num_seqs, Hq] or NULL
  *   workspace    device scratch of at least attn_decode_paged_kv4_workspace_size(...) bytes, 256-byte
  *                aligned, overwritten; two calls in flight at once need two workspaces

@@ -61,6 +61,10 @@ def append(lib, k=FAKE, v=FAKE, ks=1024, vs=1024, pool=FAKE, bt=FAKE, sl=FAKE, c
     (dict(ks=1028), ALIGN), (dict(k=FAKE + 8), ALIGN), (dict(v=FAKE + 2), ALIGN), (dict(pool=FAKE + 8), ALIGN),
     (dict(ko=FAKE + 8), ALIGN), (dict(vo=FAKE + 4), ALIGN), (dict(bt=FAKE + 2), ALIGN), (dict(cu=FAKE + 1), ALIGN),
     (dict(maxp=1 << 28), INVALID), (dict(npages=1 << 28), INVALID),
+    # outputs over inputs, other than a dense tensor over itself, or over one another
+    (dict(v=FAKE2, ko=FAKE + 16), INVALID), (dict(v=FAKE2, ks=1032, ko=FAKE), INVALID), (dict(v=FAKE2, ko=FAKE2), INVALID),
+    (dict(v=FAKE2, vo=FAKE2 - 16), INVALID), (dict(v=FAKE2, vo=FAKE), INVALID), (dict(v=FAKE2, vs=2048, vo=FAKE2), INVALID),
+    (dict(k=FAKE, v=FAKE2, ko=FAKE2 + 65536, vo=FAKE2 + 65536 + 1024), INVALID),
 ])
 def test_append_rejects_bad_arguments(lib, kw, code):
     assert append(lib, **kw) == code

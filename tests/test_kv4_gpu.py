@@ -23,6 +23,7 @@ import pytest
 import torch
 
 import attn_fwd_05_b200 as ab
+from attn_fwd_05_b200 import binding
 from oracle import attention, kv4
 
 pytestmark = pytest.mark.gpu
@@ -371,6 +372,34 @@ def test_append_special_values(cuda_device):
     assert same_values(ko, kv4.values(*kv4.quantize(f64(k)))) and same_values(vo, kv4.values(*kv4.quantize(f64(v))))
 
 
+def test_append_in_place(cuda_device):
+    # the values written back over dense k and v
+    rng = np.random.default_rng(23)
+    new, Hkv, d, ps = [5, 40, 1], 3, 128, 16
+    table, num_pages = layout(rng, new, ps)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    k, v = (bf16(rng, (sum(new), Hkv, d)).to(dev()) for _ in range(2))
+    pool = np.zeros((num_pages, Hkv, ps * d * 9 // 8), dtype=np.uint8)
+    want, ko, vo, _ = run_append(k, v, pool, table, new, cu, ps)
+    p, t, n, c = (torch.as_tensor(np.asarray(x, dtype=y)).to(dev()) for x, y in
+                  ((pool, np.uint8), (table, np.int32), (new, np.int32), (cu, np.int32)))
+    ab.attn_kv4_append(k, v, p, t, n, c, ps, k, v)
+    assert ab.attn_get_device_status() == 0
+    assert torch.equal(k, ko) and torch.equal(v, vo) and np.array_equal(p.cpu().numpy(), want)
+
+
+def test_append_looks_at_no_page_of_a_row_without_new_tokens(cuda_device):
+    rng = np.random.default_rng(24)
+    Hkv, d, ps = 2, 64, 16
+    table = np.array([[-1, -1], [0, 1], [-1, 7]], dtype=np.int32)  # rows 0 and 2 have lengths, but no pages yet
+    lens, cu = [21, 18, 30], [0, 0, 3, 3]
+    k, v = (bf16(rng, (3, Hkv, d)).to(dev()) for _ in range(2))
+    pool = np.zeros((2, Hkv, ps * d * 9 // 8), dtype=np.uint8)
+    got, _, _, status = run_append(k, v, pool, table, lens, cu, ps)
+    assert status == 0
+    assert np.array_equal(got, kv4.append(pool.copy(), f64(k), f64(v), table, lens, cu, ps))
+
+
 def test_append_errors_are_latched_and_write_nothing(cuda_device):
     rng = np.random.default_rng(24)
     d, lens, cu = 64, [20, 9], [0, 20, 29]
@@ -639,6 +668,31 @@ def test_binding_refusals(cuda_device):
     with pytest.raises(ab.AttnError):
         ab.attn_decode_paged_kv4(q, pool, table, n, 16, q, lse, -0.1, ws)
     assert ab.attn_get_device_status() == 0
+
+
+def test_tensors_of_another_device_are_refused(cuda_device, monkeypatch):
+    # with another device current, the kernels would run there on this device's addresses
+    pool = torch.zeros(4, 2, 16 * 64 * 9 // 8, dtype=torch.uint8, device=dev())
+    table, n = torch.zeros(1, 2, dtype=torch.int32, device=dev()), torch.ones(1, dtype=torch.int32, device=dev())
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=dev())
+    k, q = (torch.zeros(1, h, 64, dtype=BF, device=dev()) for h in (2, 4))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=dev())
+    pm = torch.zeros(4, dtype=torch.int32, device=dev())
+    calls = [
+        lambda: ab.attn_kv4_append(k, k, pool, table, n, cu, 16),
+        lambda: ab.attn_kv4_gather(pool, table, n, 16, k[None].transpose(1, 2).contiguous(), k[None].transpose(1, 2).contiguous()),
+        lambda: ab.attn_decode_paged_kv4(q, pool, table, n, 16, torch.empty_like(q), None, 0.1, ws),
+        lambda: ab.attn_pages_fork(table, n, torch.zeros_like(n), None, torch.empty_like(table), torch.empty_like(n), 16,
+                                   [pool], ws),
+        lambda: ab.attn_pages_compact(table, n, torch.empty_like(table), pm, 16, [pool], ws),
+    ]
+    for call in calls:
+        call()
+    assert ab.attn_get_device_status() == 0
+    monkeypatch.setattr(binding, "_current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
 
 
 @pytest.mark.parametrize("wide", [False, True])

@@ -59,6 +59,7 @@ def random_rows(rng, S, ps, cols, extra, lo=0):
 
 
 SHAPES = [((2, 16, 64), torch.bfloat16), ((2, 16, 64), torch.bfloat16)]
+LARGE = [((4, 16, 4096), torch.bfloat16)] * 4  # more to copy than a small table's one cluster takes
 
 
 @pytest.mark.parametrize("S,rows,cols,new_cols,ps,extra", [
@@ -88,10 +89,11 @@ def test_fork_chain_matches_oracle(S, rows, cols, new_cols, ps, extra, cuda_devi
             break
 
 
-def test_fork_of_a_truncated_shared_page(cuda_device):
+@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
+def test_fork_of_a_truncated_shared_page(shapes, cuda_device):
     # rows 0 and 1 share pages 0 and 1, which are full; row 0 then drops half of page 1: it must not write there
     rng = np.random.default_rng(2)
-    pools = make_pools(rng, 6, SHAPES)
+    pools = make_pools(rng, 6, shapes)
     before = raw(pools[0])
     nt, nl, left, status = run_fork([[0, 1, -1], [0, 1, 2]], [32, 40], [0, 1], [-8, 0], 3, 16, pools)
     assert status == OK and nl.tolist() == [24, 40] and nt.tolist() == [[0, 3, -1], [0, 1, 2]] and left == 2
@@ -99,18 +101,20 @@ def test_fork_of_a_truncated_shared_page(cuda_device):
     assert np.array_equal(after[3], before[1]) and np.array_equal(np.delete(after, 3, 0), np.delete(before, 3, 0))
 
 
-def test_fork_out_of_pages(cuda_device):
+@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
+def test_fork_out_of_pages(shapes, cuda_device):
     rng = np.random.default_rng(3)
-    pools = make_pools(rng, 3, SHAPES)
+    pools = make_pools(rng, 3, shapes)
     before = raw(pools[0])
     nt, nl, left, status = run_fork([[0, -1], [1, -1]], [16, 5], [0, 1, 1], [1, 0, 0], 2, 16, pools)
     assert status == TOO_LARGE and nt.tolist() == [[0, 2], [1, -1], [-1, -1]] and left == 0
     assert np.array_equal(raw(pools[0]), before)
 
 
-def test_fork_bad_inputs_are_latched(cuda_device):
+@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
+def test_fork_bad_inputs_are_latched(shapes, cuda_device):
     rng = np.random.default_rng(4)
-    pools = make_pools(rng, 8, SHAPES)
+    pools = make_pools(rng, 8, shapes)
     table, lens = [[0, 1], [2, 3]], [20, 32]
     nt, nl, _, status = run_fork(table, lens, [0, 2, -2, 1], None, 2, 16, pools)
     assert status == INVALID and nl.tolist() == [20, 0, 0, 32] and nt.tolist() == [[0, 1], [-1, -1], [-1, -1], [2, 3]]
@@ -131,7 +135,7 @@ def test_fork_bad_inputs_are_latched(cuda_device):
 
 
 @pytest.mark.parametrize("S,cols,ps,extra,shapes", [
-    (1, 1, 16, 0, SHAPES[:1]), (3, 4, 16, 20, SHAPES), (9, 3, 64, 1, [((3, 16), torch.uint8)]),
+    (1, 1, 16, 0, SHAPES[:1]), (3, 4, 16, 20, SHAPES), (9, 3, 64, 1, [((3, 16), torch.uint8)]), (3, 4, 16, 20, LARGE),
     (70, 40, 16, 3000, [((5, 48), torch.uint8)] * 4), (2000, 2, 16, 40000, [((16,), torch.uint8)]),
     (2, 3, 7, 4, [((1, 40000), torch.bfloat16)]), (4, 2, 16, 33, SHAPES),
 ])
@@ -162,9 +166,10 @@ def test_compact_matches_oracle(S, cols, ps, extra, shapes, cuda_device):
         assert np.array_equal(raw(p), b)
 
 
-def test_compact_bad_inputs_are_latched(cuda_device):
+@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
+def test_compact_bad_inputs_are_latched(shapes, cuda_device):
     rng = np.random.default_rng(6)
-    pools = make_pools(rng, 6, SHAPES)
+    pools = make_pools(rng, 6, shapes)
     ws = torch.empty(ab.attn_pages_workspace_size(6, 3), dtype=torch.uint8, device=dev())
     t, n = ints([[5, 9], [4, 1], [2, 3]]), ints([32, 20, -4])
     nt, pm, nlive = torch.empty_like(t), torch.empty(6, dtype=torch.int32, device=dev()), ints([0])
