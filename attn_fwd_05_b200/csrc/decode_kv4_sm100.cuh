@@ -19,14 +19,25 @@
 //   * fp16 range: q is scaled by a power of two per head (its bf16 significand fits fp16's);
 //     p s is scaled by a power of two per channel group that follows the largest V scale seen.
 //   * P^T reaches the B operand's layout with two 8x8 transposes (movmatrix) per group.
-//   * The running maximum is raised only when a score passes it by more than 2^8: one vote per
-//     16 tokens in place of six shuffles and a rescale.  P stays below 2^8 in between.
+//   * The running maximum is raised only when a log2 score passes it by more than 8: one vote per
+//     32 tokens in place of shuffles and a rescale.  P stays below 2^8 in between.
 //
 // Work split: the 32-token units of all (sequence, KV head, head group) segments form one
-// stream; every warp takes an equal contiguous range of it, whatever the lengths, and runs alone: it
-// fetches its records with 16-byte asynchronous copies into its own ring in shared memory and
+// stream; every warp takes a contiguous range of it of equal cost, whatever the lengths, and runs alone:
+// it fetches its records with 16-byte asynchronous copies into its own ring in shared memory and
 // never waits for another warp.  A segment that lies inside one warp's range is finished there; the
-// others leave partials (at most two per warp) that the merge kernel joins by log-sum-exp.
+// others leave partials (at most two per warp) that the merge kernel joins by log-sum-exp.  Few short
+// rows take one launch in place of two: a cluster of CTAs per segment, which joins them itself.
+//
+// What bounds it: issue slots.  A 16-token tile of 128 channels costs a warp 355 instructions (216 with
+// 64 channels), 16 of them MMAs, each of which holds its scheduler's issue port for about 8 cycles, while
+// HBM delivers a tile per scheduler every 400 cycles.  64 sequences of 512 to 32768 tokens, 64
+// query heads on 8, d = 128: 273 us, 4.9 TB/s of cache; the loads alone (no arithmetic) take 213 us,
+// without the conversion of codes 243 us.  Two rows of 131071 tokens: 76 us; 96 rows of up to 2048
+// tokens, 16 heads, d = 64: 41 us.  Tried and slower: the conversion into 8-bit operands for e4m3 MMAs
+// (this MMA becomes conversions and f16 MMAs on this GPU: 450 us), one CTA of 16 warps (no gain), and
+// tcgen05 with the codes expanded into shared memory (709 us: write, expansion and the operand's read
+// take 912 cycles of shared memory per 128 tokens, of which HBM delivers as many in 794).
 #pragma once
 
 #include "kv4_sm100.cuh"
@@ -56,18 +67,21 @@ struct DecKv4Cfg {
   static constexpr int REC = kv4_record_bytes(D);
   static constexpr int UNIT = 2 * REC;  // a unit of work: 32 tokens, two records
   static constexpr int WARPS = 4;
-  // resident CTAs: as many as the registers of the accumulators leave room for
+  // resident CTAs: as many as the registers of the accumulators leave room for (one fewer: 301 us instead
+  // of 273 for the batch above, 43 instead of 41 at d = 64)
   static constexpr int CTAS_PER_SM = D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : 2);
-  static constexpr int STAGES = (D == 64) ? 4 : 3;
+  // units in flight a warp, the one at work included: 18 KB and less (d = 256, 16 rows of up to 8192
+  // tokens: 46 us with 3 and 44 with 2; d = 128: 273 with 3, 275 with 4)
+  static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 2);
   static constexpr int SMEM = WARPS * STAGES * UNIT;
   static constexpr int THREADS = WARPS * 32;
 };
 
 constexpr int kDecKv4Unit = 2 * kKv4Tok;  // tokens of a unit
-constexpr int kDecKv4MinUnits = 2;        // shortest range of a warp, in units
+constexpr int kDecKv4MinUnits = 2;        // shortest range of a warp, in units (1 to 8 measure alike)
 constexpr int kDecKv4SegCost = 2;         // what starting and ending a segment costs, in units
 constexpr int kDecKv4MaxCluster = 8;      // most CTAs of a segment in the form for few short rows
-constexpr int kDecKv4MinCluster = 4;
+constexpr int kDecKv4MinCluster = 4;      // fewer CTAs: two launches
 constexpr int kDecKv4ClusterTokens = 1024;  // longest row it takes, per CTA of the cluster
 
 // ------------------------------------------------------------------ fp16 and copy helpers
@@ -213,7 +227,7 @@ struct Kv4Cursor {
 
 // The ranges are cut by cost: a segment of nt units counts nt + kDecKv4SegCost, the surplus in front
 // of its first unit (many short rows would otherwise make their warps the last to finish: 96 rows of
-// up to 2048 tokens with 16 heads took 60 us without it and 42 with it).
+// up to 2048 tokens with 16 heads took 59 us without it and 41 with it).
 //
 // Finds the first units of this CTA's warps: first[w] = {s, c, t, units of the range} (0 units: no
 // work).  Every thread of the block calls it.  CTA 0 also leaves the prefix of costs for the merge.
