@@ -13,6 +13,9 @@ bool kv4_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 bool cache_page_size(int p) { return p == 16 || p == 32 || p == 64; }
 
 // Sizes shared by the entry points that read a table into a 4-bit pool.  Record numbers fit an int.
+// Longest row of a table: lengths and what is rounded up from them then fit 32 bits.
+constexpr long long kMaxTokens = 1ll << 30;
+
 attn_status kv4_check(const void* pool, const int32_t* table, const int32_t* seq_lens, int page_size, int S, int Hkv,
                       int d, int num_pages, int max_pages) {
   if (S < 0 || Hkv <= 0 || num_pages < 0 || max_pages <= 0) return ATTN_ERR_INVALID_ARG;
@@ -20,7 +23,7 @@ attn_status kv4_check(const void* pool, const int32_t* table, const int32_t* seq
   if (S == 0) return ATTN_OK;
   if (table == nullptr || seq_lens == nullptr || (num_pages > 0 && pool == nullptr)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(table, 4) || !aligned(seq_lens, 4) || (num_pages > 0 && !aligned(pool, 16))) return ATTN_ERR_ALIGNMENT;
-  if ((long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > kMaxTokens) return ATTN_ERR_INVALID_ARG;
   if (num_pages > 0x7fffffffLL / Hkv / (page_size / attn::kKv4Tok)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -248,7 +251,7 @@ attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, con
   const attn_status chk =
       kv4_check(kv_pool, block_table, seq_lens, page_size, num_seqs, Hkv, d, num_pages, max_pages_per_seq);
   if (chk != ATTN_OK) return chk;
-  if (N < 0) return ATTN_ERR_INVALID_ARG;
+  if (N < 0 || N > kMaxTokens) return ATTN_ERR_INVALID_ARG;
   if (num_seqs == 0 || N == 0) return ATTN_OK;
   if (k == nullptr || v == nullptr) return ATTN_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_ALIGNMENT;
@@ -347,7 +350,8 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   if (num_seqs < 0 || new_rows < 0 || max_pages_per_seq <= 0 || new_max_pages < max_pages_per_seq || num_pages < 0 ||
       page_size <= 0)
     return ATTN_ERR_INVALID_ARG;
-  if ((long long)new_max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if ((long long)new_max_pages * page_size > kMaxTokens) return ATTN_ERR_INVALID_ARG;
+  if ((long long)new_rows * new_max_pages > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;  // pages are counted in 32 bits
   attn::PagePools pp;
   const attn_status chk = pools_check(pools, n_pools, page_bytes, num_pages, &pp);
   if (chk != ATTN_OK) return chk;
@@ -411,7 +415,7 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
                                int num_seqs, int max_pages_per_seq, int num_pages, int32_t* n_live, void* workspace,
                                size_t workspace_bytes, void* stream) {
   if (num_seqs < 0 || max_pages_per_seq <= 0 || num_pages < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
-  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages_per_seq * page_size > kMaxTokens) return ATTN_ERR_INVALID_ARG;
   attn::PagePools pp;
   const attn_status chk = pools_check(pools, n_pools, page_bytes, num_pages, &pp);
   if (chk != ATTN_OK) return chk;

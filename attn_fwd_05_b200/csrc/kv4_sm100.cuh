@@ -260,8 +260,7 @@ __global__ void __launch_bounds__(kKv4AppendThreads, NG == 1 ? 6 : (NG == 2 ? 5 
   const int c0 = __ldg(&a.cu_new[s]), c1 = __ldg(&a.cu_new[s + 1]);
   const int n = c1 - c0, len = __ldg(&a.seq_lens[s]);
   const long long qs = (long long)(c0 >> 2) + 2ll * s;
-  if (c0 < 0 || n < 0 || c1 > a.T || len < n || len > a.max_pages * a.page_size || (s == 0 && c0 != 0) ||
-      (s == a.S - 1 && c1 != a.T)) {
+  if (c0 < 0 || n < 0 || c1 > a.T || len < n || len > a.max_pages * a.page_size || (s == 0 && c0 != 0)) {
     latch_status(ATTN_ERR_INVALID_ARG);
     return;
   }

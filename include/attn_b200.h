@@ -308,7 +308,8 @@ size_t attn_decode_paged_noalloc_max_scratch(void);
  *                  4 channels of 2 tokens; nibble 4 b0 + x % 4
  *     parameters   byte 1024 NG (K) or 1088 NG (V) + 4 (((2a + b0) 2 + b1) NG + y): s in the low
  *                  half of the word, m in the high half
- * page_size is 16, 32 or 64 and d is 64, 128 or 256; num_pages * Hkv * page_size / 16 < 2^31.
+ * page_size is 16, 32 or 64 and d is 64, 128 or 256; num_pages * Hkv * page_size / 16 < 2^31,
+ * and max_pages_per_seq * page_size (like attn_kv4_gather's N) is at most 2^30.
  */
 
 /* Bytes of one page of a 4-bit pool: Hkv * page_size * d * 9 / 8, or 0 for unsupported sizes. */
@@ -323,8 +324,9 @@ size_t attn_kv4_page_bytes(int Hkv, int page_size, int d);
  *   kv_pool      device, the 4-bit pool (written: the new tokens' codes and parameters only)
  *   block_table  device, int32 [num_seqs, max_pages_per_seq], as in attn_decode_paged
  *   seq_lens     device, int32 [num_seqs]: length of each sequence WITH its new tokens
- *   cu_new       device, int32 [num_seqs + 1], increasing from 0 to num_new: rows cu_new[s] ..
- *                cu_new[s + 1] - 1 of k and v are the last tokens of sequence s
+ *   cu_new       device, int32 [num_seqs + 1], increasing from 0 to at most num_new: rows cu_new[s] ..
+ *                cu_new[s + 1] - 1 of k and v are the last tokens of sequence s; rows from
+ *                cu_new[num_seqs] on are padding, and their k_out and v_out rows are left as they were
  *   k_out, v_out device, bf16 [num_new, Hkv, d] (dense, 16-byte aligned) or NULL: written with the
  *                values the cache now stands for, rounded to bf16, so that a prompt's own attention can
  *                see exactly what later decode steps will see.  k_out may be a dense k itself and v_out a
@@ -389,7 +391,7 @@ attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int3
  *
  *   pools       HOST array of n_pools (0 .. 128) device pointers, 16-byte aligned, each to num_pages pages
  *               of page_bytes bytes (a multiple of 16); copied during the call
- *   page_size   tokens per page (any positive number)
+ *   page_size   tokens per page (any positive number; a row's pages hold at most 2^30 tokens)
  *
  * attn_pages_workspace_size — scratch of attn_pages_fork (rows = new_rows) and attn_pages_compact
  * (rows = num_seqs): 256-byte aligned, needs no initialisation, one per call in flight.

@@ -60,7 +60,7 @@ def append(lib, k=FAKE, v=FAKE, ks=1024, vs=1024, pool=FAKE, bt=FAKE, sl=FAKE, c
     (dict(bt=None), INVALID), (dict(sl=None), INVALID), (dict(ks=1016), INVALID), (dict(vs=8), INVALID),
     (dict(ks=1028), ALIGN), (dict(k=FAKE + 8), ALIGN), (dict(v=FAKE + 2), ALIGN), (dict(pool=FAKE + 8), ALIGN),
     (dict(ko=FAKE + 8), ALIGN), (dict(vo=FAKE + 4), ALIGN), (dict(bt=FAKE + 2), ALIGN), (dict(cu=FAKE + 1), ALIGN),
-    (dict(maxp=1 << 28), INVALID), (dict(npages=1 << 28), INVALID),
+    (dict(maxp=1 << 28), INVALID), (dict(maxp=(1 << 26) + 1), INVALID), (dict(npages=1 << 28), INVALID),
     # outputs over inputs, other than a dense tensor over itself, or over one another
     (dict(v=FAKE2, ko=FAKE + 16), INVALID), (dict(v=FAKE2, ks=1032, ko=FAKE), INVALID), (dict(v=FAKE2, ko=FAKE2), INVALID),
     (dict(v=FAKE2, vo=FAKE2 - 16), INVALID), (dict(v=FAKE2, vo=FAKE), INVALID), (dict(v=FAKE2, vs=2048, vo=FAKE2), INVALID),
@@ -83,6 +83,7 @@ def gather(lib, pool=FAKE, bt=FAKE, sl=FAKE, ps=16, k=FAKE, v=FAKE, S=4, Hkv=8, 
     (dict(S=-1), INVALID), (dict(N=-1), INVALID), (dict(Hkv=0), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(k=FAKE + 8), ALIGN), (dict(v=FAKE + 8), ALIGN), (dict(pool=FAKE + 4), ALIGN), (dict(d=80), UNSUPPORTED),
     (dict(ps=128), UNSUPPORTED), (dict(pool=None), INVALID), (dict(sl=None), INVALID),
+    (dict(N=(1 << 30) + 1), INVALID), (dict(maxp=(1 << 26) + 1), INVALID),
 ])
 def test_gather_rejects_bad_arguments(lib, kw, code):
     assert gather(lib, **kw) == code
@@ -105,7 +106,7 @@ def dec(lib, q=FAKE, pool=FAKE, bt=FAKE, sl=FAKE, ps=16, o=FAKE, lse=None, S=4, 
     (dict(o=None), INVALID), (dict(bt=None), INVALID), (dict(sl=None), INVALID), (dict(pool=None), INVALID),
     (dict(q=FAKE + 8), ALIGN), (dict(o=FAKE + 4), ALIGN), (dict(pool=FAKE + 8), ALIGN), (dict(lse=FAKE + 2), ALIGN),
     (dict(ws=FAKE + 16), ALIGN), (dict(ws=None), WORKSPACE), (dict(wsb=100), WORKSPACE),
-    (dict(S=100000, maxp=1 << 20), INVALID), (dict(S=1 << 14, maxp=1 << 18), INVALID),  # 2^31 units of 32 tokens
+    (dict(maxp=(1 << 26) + 1), INVALID), (dict(S=100000, maxp=1 << 20), INVALID), (dict(S=1 << 14, maxp=1 << 18), INVALID),  # 2^31 units of 32 tokens
 ])
 def test_decode_rejects_bad_arguments(lib, kw, code):
     assert dec(lib, **kw) == code
@@ -130,7 +131,8 @@ def fork(lib, bt=FAKE, sl=FAKE, parents=FAKE + 4096, add=None, nt=FAKE2, nl=FAKE
 
 @pytest.mark.parametrize("kw,code", [
     (dict(S=-1), INVALID), (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(ncols=7), INVALID),
-    (dict(npages=-1), INVALID), (dict(ps=0), INVALID), (dict(ncols=1 << 28), INVALID), (dict(pb=4088), INVALID),
+    (dict(npages=-1), INVALID), (dict(ps=0), INVALID), (dict(ncols=1 << 28), INVALID), (dict(ps=(1 << 27) + 1), INVALID),
+    (dict(rows=1 << 20, ncols=1 << 12), INVALID), (dict(pb=4088), INVALID),
     (dict(pools=None, n=1), INVALID), (dict(n=-1), INVALID), (dict(n=129), TOO_LARGE), (dict(pools=(FAKE, None)), INVALID),
     (dict(pools=(FAKE + 8,)), ALIGN), (dict(bt=None), INVALID), (dict(sl=None), INVALID), (dict(parents=None), INVALID),
     (dict(nt=None), INVALID), (dict(nl=None), INVALID), (dict(bt=FAKE + 2), ALIGN), (dict(nfree=FAKE + 2), ALIGN),
@@ -151,7 +153,8 @@ def compact(lib, bt=FAKE, sl=FAKE, nt=FAKE2, pm=FAKE2 + 65536, ps=16, pools=(FAK
 @pytest.mark.parametrize("kw,code", [
     (dict(S=-1), INVALID), (dict(cols=0), INVALID), (dict(npages=-1), INVALID), (dict(ps=-16), INVALID),
     (dict(pb=8), INVALID), (dict(n=129), TOO_LARGE), (dict(pools=(None,)), INVALID), (dict(pools=(FAKE + 4,)), ALIGN),
-    (dict(bt=None), INVALID), (dict(nt=None), INVALID), (dict(pm=None), INVALID), (dict(nt=FAKE + 16), INVALID),
+    (dict(ps=(1 << 27) + 1), INVALID), (dict(bt=None), INVALID), (dict(nt=None), INVALID), (dict(pm=None), INVALID),
+    (dict(nt=FAKE + 16), INVALID),
     (dict(pm=FAKE + 2), ALIGN), (dict(ws=None), WORKSPACE), (dict(wsb=100), WORKSPACE), (dict(ws=FAKE + 128), ALIGN),
 ])
 def test_compact_rejects_bad_arguments(lib, kw, code):

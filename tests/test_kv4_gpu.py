@@ -388,6 +388,23 @@ def test_append_in_place(cuda_device):
     assert torch.equal(k, ko) and torch.equal(v, vo) and np.array_equal(p.cpu().numpy(), want)
 
 
+def test_append_of_a_padded_batch(cuda_device):
+    # 12 rows of k and v of which three sequences have 6; the rest is padding
+    rng = np.random.default_rng(25)
+    Hkv, d, ps = 2, 128, 16
+    lens, cu = [17, 0, 4, 9], [0, 1, 1, 5, 6]
+    table, num_pages = layout(rng, lens, ps)
+    k, v = (bf16(rng, (12, Hkv, d)).to(dev()) for _ in range(2))
+    k[6:], v[6:] = float("nan"), float("inf")
+    pool = rng.integers(0, 256, (num_pages, Hkv, ps * d * 9 // 8), dtype=np.uint8)
+    got, ko, vo, status = run_append(k, v, pool, table, lens, cu, ps)
+    assert status == 0
+    assert np.array_equal(got, kv4.append(pool, f64(k[:6]), f64(v[:6]), table, lens, cu, ps))
+    assert same_values(ko[:6], kv4.values(*kv4.quantize(f64(k[:6])))) and same_values(vo[:6], kv4.values(*kv4.quantize(f64(v[:6]))))
+    untouched = bf16_bits_of(torch.full((1,), float("nan"), dtype=BF))[0]
+    assert (bf16_bits_of(ko[6:]) == untouched).all() and (bf16_bits_of(vo[6:]) == untouched).all()
+
+
 def test_append_looks_at_no_page_of_a_row_without_new_tokens(cuda_device):
     rng = np.random.default_rng(24)
     Hkv, d, ps = 2, 64, 16
@@ -418,7 +435,7 @@ def test_append_errors_are_latched_and_write_nothing(cuda_device):
         page = ok[good, 0]
         assert np.array_equal(got[page], want[page])
         assert np.array_equal(np.delete(got, [page, 2], 0), np.delete(pool, [page, 2], 0))
-    for bad_cu in ([0, 20, 28], [1, 20, 29], [0, 30, 29], [0, -5, 29]):
+    for bad_cu in ([0, 20, 30], [1, 20, 29], [0, 30, 29], [0, -5, 29]):
         got, _, _, status = run_append(k, v, pool, ok, lens, bad_cu, 16)
         assert status == 1
 
