@@ -165,7 +165,7 @@ __device__ __forceinline__ void fork_row_done(const ForkArgs& a, int i, int4 row
   a.row_fresh[i] = (row.w + a.page_size - 1) / a.page_size - row.y - row.z;
 }
 
-// Lists the free pages in ascending order and gives each row its rank in that list.  lowest(i, e): row
+// Lists the free pages that are needed, in ascending order, and gives each row its rank in that list.  lowest(i, e): row
 // i is the lowest with the part-filled page e.  Such a page stays with the lowest row that has it,
 // unless some row has it as a full page (that row's tokens must not be written over).
 template <typename Lowest>
@@ -197,8 +197,9 @@ __device__ __forceinline__ void fork_rank(const ForkArgs& a, const volatile uint
   }
   int2 total;
   int2 at = pages_scan(mine, sums, &total);
-  for (int w = w0; w < w1; ++w)
-    for (uint32_t f = free_bits(w); f != 0; f &= f - 1) a.free_list[at.x++] = 32 * w + __ffs(f) - 1;
+  // only the pages that rows will take: writing all 65 thousand of an empty pool took 34 us
+  for (int w = w0; w < w1 && at.x < total.y; ++w)
+    for (uint32_t f = free_bits(w); f != 0 && at.x < total.y; f &= f - 1) a.free_list[at.x++] = 32 * w + __ffs(f) - 1;
   for (int i = i0; i < i1; ++i) {
     a.row_rank[i] = at.y;
     at.y += row_fresh[i] + (row_part[i] >= 0 && !a.row_keep[i] ? 1 : 0);
