@@ -169,13 +169,18 @@ int copy_parts(size_t page_bytes) {
   return (int)std::max<size_t>(1, std::min<size_t>(32, page_bytes / 16384));
 }
 
-// One launch of one cluster is cheaper than a clearing and two kernels (8 rows of 64 pages: fork 7.1 us
-// instead of 9.3, compact 7.6 instead of 10.3) while one CTA plans the entries in a round or two (16 x
-// 128: 10.1 and 11.5 us against 11.9 and 12.3; 32 x 128: 14.4 and 16.9 against 13.7 and 14.3) and 8 CTAs
-// copy at most `bytes` (8 forked rows of 128 KB pages: 10.1 us against 12.3; 64 of 32 KB: 16.0 against 12.3).
-bool small_table(int rows, int cols, int num_pages, double copies, const attn::PagePools& pp, long long bytes) {
-  return rows <= attn::kSmallRows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages &&
-         copies * pp.n * (double)pp.page_bytes <= (double)bytes;
+// One CTA that plans saves the clearing and a launch, while it has few entries and rows to walk.  Fork /
+// compact in microseconds against clearing and a CTA a row: 8 x 64 entries 6.5 / 7.6 against 9.6 / 12.3, 16
+// x 128 8.8 / 11.3 against 10.7 / 12.3, 32 x 128 11.7 / 15.8 against 11.3 / 14.3; 256 x 8 19.9 / 10.1 against
+// 11.5 / 12.3 (a fork compares the rows' part-filled pages with one another).
+bool small_table(int rows, int max_rows, int cols, int num_pages) {
+  return rows <= max_rows && (long long)rows * cols <= attn::kSmallEntries && num_pages <= attn::kSmallPages;
+}
+
+// Whether the planning launch also copies: at most `bytes`, for which the 8 CTAs of a cluster are enough (256
+// pages of 16 KB that could move, 4 MB: 10.9 us against 12.3; of 32 KB: 16.2).
+int small_move(double copies, const attn::PagePools& pp, long long bytes) {
+  return copies * pp.n * (double)pp.page_bytes <= (double)bytes;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -399,12 +404,16 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   a.page_size = page_size;
   a.num_pages = num_pages;
   const int parts = copy_parts(page_bytes);
-  if (small_table(new_rows, new_max_pages, num_pages, new_rows, pp, attn::kSmallForkBytes))
-    return launch_cluster(attn::attn_pages_fork_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster,
-                          attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 8, st, a, pp);
-  if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
-  attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (small_table(new_rows, attn::kSmallForkRows, new_max_pages, num_pages)) {
+    const int move = small_move(new_rows, pp, attn::kSmallForkBytes), ctas = move ? attn::kSmallCluster : 1;
+    const attn_status planned = launch_cluster(attn::attn_pages_fork_small_kernel, dim3(ctas), ctas, attn::kPlanThreads,
+                                               (size_t)((num_pages + 31) / 32) * 8, st, a, pp, move);
+    if (planned != ATTN_OK || move) return planned;
+  } else {
+    if (cudaMemsetAsync(ws, 0, L.zero_first, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    attn::attn_pages_fork_plan_kernel<<<(unsigned)std::max(new_rows, 1), attn::kPlanThreads, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  }
   if (new_rows == 0) return ATTN_OK;
   const dim3 grid((unsigned)new_rows, (unsigned)std::max(1, std::min(pp.n * parts, 1024)));
   return launch_dependent(attn::attn_pages_fork_move_kernel, grid, attn::kPagesThreads, st, a, pp, parts);
@@ -452,12 +461,16 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   const int parts = copy_parts(page_bytes);
   // a page moves into a free one, so at most half of the pool moves
   const double moves = std::min((double)num_seqs * max_pages_per_seq, num_pages / 2.0);
-  if (small_table(num_seqs, max_pages_per_seq, num_pages, moves, pp, attn::kSmallCompactBytes))
-    return launch_cluster(attn::attn_pages_compact_small_kernel, dim3(attn::kSmallCluster), attn::kSmallCluster,
-                          attn::kPlanThreads, (size_t)((num_pages + 31) / 32) * 4, st, a, pp);
-  if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
-  attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (small_table(num_seqs, attn::kSmallCompactRows, max_pages_per_seq, num_pages)) {
+    const int move = small_move(moves, pp, attn::kSmallCompactBytes), ctas = move ? attn::kSmallCluster : 1;
+    const attn_status planned = launch_cluster(attn::attn_pages_compact_small_kernel, dim3(ctas), ctas, attn::kPlanThreads,
+                                               (size_t)((num_pages + 31) / 32) * 4, st, a, pp, move);
+    if (planned != ATTN_OK || move) return planned;
+  } else {
+    if (cudaMemsetAsync(ws, 0, L.zero_bytes, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    attn::attn_pages_compact_plan_kernel<<<(unsigned)std::max(num_seqs, 1), attn::kPlanThreads, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  }
   return launch_dependent(attn::attn_pages_compact_move_kernel, dim3((unsigned)(sm_count() * 8)), attn::kPagesThreads,
                           st, a, pp, parts);
 }

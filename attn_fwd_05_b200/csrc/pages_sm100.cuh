@@ -8,11 +8,11 @@
 //   plan   the rows' pages set bits of a map over the pool (many CTAs, one row each); the CTA that
 //          finishes last ranks the free pages (fork) or the moves (compact) with popcounts and
 //          one block-wide scan.  Ranks make the result independent of the order of execution.
-//          A small table is planned and moved in one launch by one cluster, with the map in shared
-//          memory and nothing to clear.
+//          A small table is planned by one CTA, with the map in shared memory and nothing to clear;
+//          where there is little to copy, its cluster does that too, in the same launch.
 //   move   many CTAs write the table and copy pages with 16-byte loads and stores
 // Integer work on a few KB is bound by the latency of the launches and of the scan: 4 rows of 70
-// pages, one page copied, 8.3 us as one cluster, 10.2 as one planning CTA and a move kernel, 13.0 with the
+// pages, one page copied, 8.3 us as one cluster, 10.2 as one planning CTA and a move kernel, 11.9 with the
 // clearing and many planning CTAs.  The copies are bound by HBM (each byte read once and written once):
 // 0.73 GB of pages moved take 260 us, 5.6 TB/s.
 #pragma once
@@ -105,8 +105,8 @@ __device__ __forceinline__ int2 pages_scan(int2 v, int2* sums, int2* total) {
   return before;
 }
 
-// Tables handled by one cluster: up to this many entries, rows and pages, and bytes to copy at most.
-constexpr int kSmallEntries = 2048, kSmallRows = 32, kSmallPages = 65536, kSmallCluster = 8;
+// Tables planned by one CTA: up to this many entries, rows and pages; and bytes that its cluster copies.
+constexpr int kSmallEntries = 2048, kSmallForkRows = 32, kSmallCompactRows = 256, kSmallPages = 65536, kSmallCluster = 8;
 constexpr long long kSmallForkBytes = 1ll << 20;     // every row's part-filled page
 constexpr long long kSmallCompactBytes = 4ll << 20;  // what could move; most often half of it does
 
@@ -298,13 +298,13 @@ __global__ void __launch_bounds__(kPagesThreads)
   }
 }
 
-// A small table in one launch of one cluster: its first CTA plans with the maps in (dynamic) shared
-// memory while the others wait at the cluster's barrier, then all of them move.
+// A small table.  The first CTA plans with the maps in (dynamic) shared memory.  For `move` the grid is one
+// cluster, whose other CTAs wait at its barrier, and all of them move; else it is that one CTA.
 __global__ void __launch_bounds__(kPlanThreads)
-    attn_pages_fork_small_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PagePools pools) {
+    attn_pages_fork_small_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PagePools pools, int move) {
   extern __shared__ uint32_t maps[];
   __shared__ int2 sums[kPlanThreads / 32];
-  __shared__ int4 rows[kSmallRows];
+  __shared__ int4 rows[kSmallForkRows];
   if (blockIdx.x == 0) {
     const int words = (a.num_pages + 31) / 32;
     uint32_t *full = maps, *part = maps + words;
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     };
     fork_rank(a, full, part, lowest, sums);
   }
+  if (!move) return pdl_launch_dependents();
   cluster_barrier();
   const int warp = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kPlanThreads / 32);
   const int n_list = *a.n_list;
@@ -478,12 +479,13 @@ __global__ void __launch_bounds__(kPagesThreads)
   }
 }
 
-// A small table in one launch of one cluster, as for the fork.
+// A small table, as for the fork.
 __global__ void __launch_bounds__(kPlanThreads)
-    attn_pages_compact_small_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PagePools pools) {
+    attn_pages_compact_small_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PagePools pools,
+                                    int move) {
   extern __shared__ uint32_t maps[];
   __shared__ int2 sums[kPlanThreads / 32];
-  __shared__ int used[kSmallRows];
+  __shared__ int used[kSmallCompactRows];
   if (blockIdx.x == 0) {
     const int words = (a.num_pages + 31) / 32;
     for (int w = threadIdx.x; w < words; w += kPlanThreads) maps[w] = 0;
@@ -498,6 +500,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
     compact_rank(a, maps, sums);
   }
+  if (!move) return pdl_launch_dependents();
   cluster_barrier();
   const int live = a.counts[0], n_move = a.counts[1];
   compact_write(a, live, n_move);

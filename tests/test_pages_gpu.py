@@ -33,8 +33,15 @@ def raw(p):
     return p.contiguous().view(torch.uint8).reshape(p.shape[0], -1).cpu().numpy()
 
 
-def run_fork(table, lens, parents, add, new_cols, ps, pools, n_free=True):
+def widened(table, more):
+    t = np.asarray(table, dtype=np.int32)
+    return np.concatenate([t, np.full((t.shape[0], more), -1, dtype=np.int32)], axis=1)
+
+
+def run_fork(table, lens, parents, add, new_cols, ps, pools, n_free=True, more=0):
+    """more: columns that no row fills."""
     rows = len(parents)
+    table, new_cols = widened(table, more), new_cols + more
     nt = torch.full((rows, new_cols), 77, dtype=torch.int32, device=dev())
     nl = torch.full((rows,), 77, dtype=torch.int32, device=dev())
     left = ints([77]) if n_free else None
@@ -42,7 +49,9 @@ def run_fork(table, lens, parents, add, new_cols, ps, pools, n_free=True):
     ab.attn_pages_fork(ints(table), ints(lens), ints(parents), None if add is None else ints(add), nt, nl, ps, pools, ws,
                        left)
     status = ab.attn_get_device_status()
-    return nt.cpu().numpy(), nl.cpu().numpy(), None if left is None else int(left), status
+    nt = nt.cpu().numpy()
+    assert (nt[:, new_cols - more:] == -1).all()
+    return nt[:, :new_cols - more], nl.cpu().numpy(), None if left is None else int(left), status
 
 
 def random_rows(rng, S, ps, cols, extra, lo=0):
@@ -59,7 +68,8 @@ def random_rows(rng, S, ps, cols, extra, lo=0):
 
 
 SHAPES = [((2, 16, 64), torch.bfloat16), ((2, 16, 64), torch.bfloat16)]
-LARGE = [((4, 16, 4096), torch.bfloat16)] * 4  # more to copy than a small table's one cluster takes
+LARGE = [((4, 16, 4096), torch.bfloat16)] * 4  # more to copy than the planning launch takes
+PLANS = [(SHAPES, 0), (LARGE, 0), (SHAPES, 2100)]  # and more entries than one CTA plans
 
 
 @pytest.mark.parametrize("S,rows,cols,new_cols,ps,extra", [
@@ -89,48 +99,48 @@ def test_fork_chain_matches_oracle(S, rows, cols, new_cols, ps, extra, cuda_devi
             break
 
 
-@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
-def test_fork_of_a_truncated_shared_page(shapes, cuda_device):
+@pytest.mark.parametrize("shapes,more", PLANS)
+def test_fork_of_a_truncated_shared_page(shapes, more, cuda_device):
     # rows 0 and 1 share pages 0 and 1, which are full; row 0 then drops half of page 1: it must not write there
     rng = np.random.default_rng(2)
     pools = make_pools(rng, 6, shapes)
     before = raw(pools[0])
-    nt, nl, left, status = run_fork([[0, 1, -1], [0, 1, 2]], [32, 40], [0, 1], [-8, 0], 3, 16, pools)
+    nt, nl, left, status = run_fork([[0, 1, -1], [0, 1, 2]], [32, 40], [0, 1], [-8, 0], 3, 16, pools, more=more)
     assert status == OK and nl.tolist() == [24, 40] and nt.tolist() == [[0, 3, -1], [0, 1, 2]] and left == 2
     after = raw(pools[0])
     assert np.array_equal(after[3], before[1]) and np.array_equal(np.delete(after, 3, 0), np.delete(before, 3, 0))
 
 
-@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
-def test_fork_out_of_pages(shapes, cuda_device):
+@pytest.mark.parametrize("shapes,more", PLANS)
+def test_fork_out_of_pages(shapes, more, cuda_device):
     rng = np.random.default_rng(3)
     pools = make_pools(rng, 3, shapes)
     before = raw(pools[0])
-    nt, nl, left, status = run_fork([[0, -1], [1, -1]], [16, 5], [0, 1, 1], [1, 0, 0], 2, 16, pools)
+    nt, nl, left, status = run_fork([[0, -1], [1, -1]], [16, 5], [0, 1, 1], [1, 0, 0], 2, 16, pools, more=more)
     assert status == TOO_LARGE and nt.tolist() == [[0, 2], [1, -1], [-1, -1]] and left == 0
     assert np.array_equal(raw(pools[0]), before)
 
 
-@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
-def test_fork_bad_inputs_are_latched(shapes, cuda_device):
+@pytest.mark.parametrize("shapes,more", PLANS)
+def test_fork_bad_inputs_are_latched(shapes, more, cuda_device):
     rng = np.random.default_rng(4)
     pools = make_pools(rng, 8, shapes)
     table, lens = [[0, 1], [2, 3]], [20, 32]
-    nt, nl, _, status = run_fork(table, lens, [0, 2, -2, 1], None, 2, 16, pools)
+    nt, nl, _, status = run_fork(table, lens, [0, 2, -2, 1], None, 2, 16, pools, more=more)
     assert status == INVALID and nl.tolist() == [20, 0, 0, 32] and nt.tolist() == [[0, 1], [-1, -1], [-1, -1], [2, 3]]
-    nt, nl, _, status = run_fork(table, lens, [0, 1], [-21, 1], 2, 16, pools)
+    nt, nl, _, status = run_fork(table, lens, [0, 1], [-21, 1 + 16 * more], 2, 16, pools, more=more)
     assert status == INVALID and nl.tolist() == [20, 32] and nt.tolist() == [[0, 1], [2, 3]]
-    nt, nl, _, status = run_fork(table, [-3, 33], [0, 1], [4, 0], 2, 16, pools)
+    nt, nl, _, status = run_fork(table, [-3, 33 + 16 * more], [0, 1], [4, 0], 2, 16, pools, more=more)
     assert status == INVALID and nl.tolist() == [4, 0] and nt.tolist() == [[0, -1], [-1, -1]]
     before = raw(pools[0])
-    nt, nl, _, status = run_fork([[8, 1], [2, -1]], lens, [0, 1, 0], None, 2, 16, pools)
+    nt, nl, _, status = run_fork([[8, 1], [2, -1]], lens, [0, 1, 0], None, 2, 16, pools, more=more)
     assert status == BAD_PAGE and nt.tolist() == [[-1, 1], [2, -1], [-1, 0]]
     after = raw(pools[0])
     assert np.array_equal(after[0], before[1]) and np.array_equal(after[1:], before[1:])
     # a part-filled page out of range: nothing to copy
-    nt, nl, _, status = run_fork([[0, 99], [2, 3]], lens, [0, 0], None, 2, 16, pools)
+    nt, nl, _, status = run_fork([[0, 99], [2, 3]], lens, [0, 0], None, 2, 16, pools, more=more)
     assert status == BAD_PAGE and nt.tolist() == [[0, -1], [0, -1]]
-    nt, nl, left, status = run_fork(table, lens, [], None, 2, 16, pools)
+    nt, nl, left, status = run_fork(table, lens, [], None, 2, 16, pools, more=more)
     assert status == OK and left == 8
 
 
@@ -166,16 +176,16 @@ def test_compact_matches_oracle(S, cols, ps, extra, shapes, cuda_device):
         assert np.array_equal(raw(p), b)
 
 
-@pytest.mark.parametrize("shapes", [SHAPES, LARGE])
-def test_compact_bad_inputs_are_latched(shapes, cuda_device):
+@pytest.mark.parametrize("shapes,more", PLANS)
+def test_compact_bad_inputs_are_latched(shapes, more, cuda_device):
     rng = np.random.default_rng(6)
     pools = make_pools(rng, 6, shapes)
     ws = torch.empty(ab.attn_pages_workspace_size(6, 3), dtype=torch.uint8, device=dev())
-    t, n = ints([[5, 9], [4, 1], [2, 3]]), ints([32, 20, -4])
+    t, n = ints(widened([[5, 9], [4, 1], [2, 3]], more)), ints([32, 20, -4])
     nt, pm, nlive = torch.empty_like(t), torch.empty(6, dtype=torch.int32, device=dev()), ints([0])
     ab.attn_pages_compact(t, n, nt, pm, 16, pools, ws, nlive)
     assert ab.attn_get_device_status() in (INVALID, BAD_PAGE)
-    assert nt.tolist() == [[2, -1], [0, 1], [-1, -1]] and int(nlive) == 3 and pm.tolist() == [-1, 1, -1, -1, 0, 2]
+    assert nt[:, :2].tolist() == [[2, -1], [0, 1], [-1, -1]] and (nt[:, 2:] == -1).all() and int(nlive) == 3 and pm.tolist() == [-1, 1, -1, -1, 0, 2]
 
 
 def test_pages_without_rows_or_pools_of_no_pages(cuda_device):
