@@ -266,6 +266,22 @@ def test_decode_nan_groups_stay_in_their_rows(wide, cuda_device):
 
 
 @pytest.mark.parametrize("wide", [False, True])
+def test_decode_queries_that_are_not_finite_stay_in_their_heads(wide, cuda_device):
+    rng = np.random.default_rng(12)
+    lens = [500, 40]
+    table, num_pages = layout(rng, lens, 16)
+    pool = random_pool(rng, num_pages, 1, 16, 64)
+    q = bf16(rng, (2, 5, 64))
+    q[0, 1], q[1, 3, 7] = float("nan"), float("inf")
+    o, lse, status = run_decode(q, pool, widen(table, 16) if wide else table, lens, 16, 0.125)
+    assert status == 0
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(lse[0, 1]) and not torch.isfinite(o[1, 3]).any()
+    for row, rest in ((0, [0, 2, 3, 4]), (1, [0, 1, 2, 4])):
+        check_decode(o[row:row + 1, rest], lse[row:row + 1, rest], q[row:row + 1, rest], pool, table[row:row + 1],
+                     lens[row:row + 1], 16, 0.125)
+
+
+@pytest.mark.parametrize("wide", [False, True])
 def test_decode_bad_pages_and_lengths_are_reported(wide, cuda_device):
     rng = np.random.default_rng(10)
     lens = [100, 50, 64]

@@ -220,3 +220,51 @@ def test_binding_refusals(cuda_device):
     with pytest.raises(ab.AttnError):
         ab.attn_pages_compact(t, n, nt, pm, 16, pools, ws[:256])
     assert ab.attn_get_device_status() == OK
+
+
+@pytest.mark.parametrize("more", [0, 2100])
+def test_bf16_cache_forked_compacted_and_decoded_in_a_graph(more, cuda_device):
+    # K and V pools of attn_decode_paged: every row of the new table answers as its parent did, bit for bit
+    rng = np.random.default_rng(31 + more)
+    ps, Hkv, Hq, d = 16, 2, 8, 128
+    table, lens, num_pages = random_rows(rng, 4, ps, 40, 30, lo=1)
+    fill = [torch.randn((num_pages, Hkv, ps, d), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16) for i in range(2)]
+    pools = [f.to(dev()) for f in fill]
+    parents = [2, 0, 0, 3, 1, 0]
+    q0 = torch.randn((4, Hq, d), generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(dev())
+    q = q0[parents].contiguous()
+    t, n, cols = ints(widened(table, more)), ints(lens), 40 + more
+
+    def decode(q, table, lens, o, lse, ws):
+        ab.attn_decode_paged(q, pools[0], pools[1], table, lens, ps, o, lse, 0.09, ws)
+
+    def outputs(rows):
+        return (torch.empty((rows, Hq, d), dtype=torch.bfloat16, device=dev()),
+                torch.empty((rows, Hq), dtype=torch.float32, device=dev()),
+                torch.empty(ab.attn_decode_paged_workspace_size(rows, Hq, Hkv, d, cols, ps), dtype=torch.uint8, device=dev()))
+
+    o0, l0, ws0 = outputs(4)
+    decode(q0, t, n, o0, l0, ws0)
+    o, lse, ws = outputs(6)
+    nt, nl = torch.empty((6, cols), dtype=torch.int32, device=dev()), torch.empty(6, dtype=torch.int32, device=dev())
+    pm, par = torch.empty(num_pages, dtype=torch.int32, device=dev()), ints(parents)
+    pws = torch.empty(ab.attn_pages_workspace_size(num_pages, 6), dtype=torch.uint8, device=dev())
+
+    def step():
+        ab.attn_pages_fork(t, n, par, None, nt, nl, ps, pools, pws)
+        ab.attn_pages_compact(nt, nl, nt, pm, ps, pools, pws)
+        decode(q, nt, nl, o, lse, ws)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for replay in range(3):
+        for p, f in zip(pools, fill):
+            p.copy_(f)
+        for x in (o, lse, nt, nl, pm):
+            x.zero_()
+        pws.fill_(0x5A)
+        g.replay() if replay else step()
+        assert ab.attn_get_device_status() == OK
+        assert torch.equal(o, o0[parents]) and torch.equal(lse, l0[parents])
+    del g
