@@ -67,8 +67,8 @@ struct DecKv4Cfg {
   static constexpr int REC = kv4_record_bytes(D);
   static constexpr int UNIT = 2 * REC;  // a unit of work: 32 tokens, two records
   static constexpr int WARPS = 4;
-  // resident CTAs: as many as the registers of the accumulators leave room for (one fewer: 301 us instead
-  // of 273 for the batch above, 43 instead of 41 at d = 64)
+  // resident CTAs (one fewer: 301 us instead of 273 for the batch above, 43 instead of 41 at d = 64; one
+  // more, squeezed into 128 and 96 registers: 282 against 281, two long rows 80 against 76, 43 against 41)
   static constexpr int CTAS_PER_SM = D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : 2);
   // units in flight a warp, the one at work included: 18 KB and less (d = 256, 16 rows of up to 8192
   // tokens: 46 us with 3 and 44 with 2; d = 128: 273 with 3, 275 with 4)
