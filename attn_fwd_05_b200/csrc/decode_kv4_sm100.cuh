@@ -17,7 +17,8 @@
 //     Centring the codes keeps the rounding of p s (fp16, 11 bits) multiplied by the small signed
 //     code instead of by an offset that the second sum would have to cancel.
 //   * fp16 range: q is scaled by a power of two per head (its bf16 significand fits fp16's);
-//     p s is scaled by a power of two per channel group that follows the largest V scale seen.
+//     p s is scaled by a power of two per head and channel group that follows the largest p s seen, not the
+//     largest s: a token of a large scale and no weight would push the others into fp16's subnormals.
 //   * P^T reaches the B operand's layout with two 8x8 transposes (movmatrix) per group.
 //   * The running maximum is raised only when a log2 score passes it by more than 8: one vote per
 //     32 tokens in place of shuffles and a rescale.  P stays below 2^8 in between.
@@ -148,11 +149,19 @@ __device__ __forceinline__ void sts_word(uint32_t addr, uint32_t w) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+// Larger of two pairs of fp16 numbers; NaN where either is.
+__device__ __forceinline__ uint32_t max_nan_f16x2(uint32_t a, uint32_t b) {
   uint32_t c;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
   return c;
 }
+
+// A pair of bf16 powers of two 2^-e (halves: two query heads), -120 <= e <= 120.
+__device__ __forceinline__ int unit_exponent(uint32_t u, int half) { return 127 - (int)((u >> (16 * half + 7)) & 0xffu); }
+__device__ __forceinline__ uint32_t unit_pair(int e0, int e1) {
+  return (uint32_t)(127 - e0) << 7 | (uint32_t)(127 - e1) << 23;
+}
+constexpr int kDecKv4UnitMin = -120, kDecKv4UnitMax = 120;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -179,10 +188,10 @@ __device__ __forceinline__ void kv4_centred(uint32_t w, uint32_t (&p)[4]) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// Exponent of x >= 0, clamped to [-100, top]; of 0 the lower end, of infinity and NaN (which any
+// Exponent of x >= 0, clamped to [low, top]; of 0 the lower end, of infinity and NaN (which any
 // scaling keeps) the upper end.
-__device__ __forceinline__ int exponent_of(float x, int top) {
-  return min(top, max(-100, (int)((__float_as_uint(x) >> 23) & 0xffu) - 127));
+__device__ __forceinline__ int exponent_of(float x, int low, int top) {
+  return min(top, max(low, (int)((__float_as_uint(x) >> 23) & 0xffu) - 127));
 }
 
 __device__ __forceinline__ float max_over_rows(float x) {  // over the 8 rows of an MMA fragment column
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
   float l[NT][2];               // sum of exponentials (this lane's tokens)
   float zs[NT][NG][2];          // sum of p (m + 8 s) (this lane's tokens)
   float oc[NT][NG * 4][4];      // O^T / 2^es: rows 8g + 2mt (+1), heads 2t, 2t + 1
-  float unit[NG];               // 2^-es, what the V scales of a group are multiplied by
+  uint32_t unit[NT][NG];        // 2^-es of heads 2t and 2t + 1, what p s is multiplied by
   auto head_of = [&](int c) -> int { return c / a.n_hg * a.group + c % a.n_hg * C::ROWS; };
   auto rows_of = [&](int c) -> int { return min(C::ROWS, a.group - c % a.n_hg * C::ROWS); };
   auto begin = [&]() {
@@ -468,7 +477,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
       // largest element to [2^13, 2^14): fp16 then holds every element down to 2^-31 of it exactly
-      const int e = exponent_of(__uint_as_float(big), 127) - 13;
+      const int e = exponent_of(__uint_as_float(big), -100, 127) - 13;
       const float down = pow2i(-e);
 #pragma unroll
       for (int ks = 0; ks < NG * 4; ++ks) {
@@ -489,14 +498,13 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
         qs[nt][y][0] = s4[0];
         qs[nt][y][1] = s4[1];
         zs[nt][y][0] = zs[nt][y][1] = 0.f;
+        unit[nt][y] = unit_pair(kDecKv4UnitMin, kDecKv4UnitMin);
       }
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < NG * 4; ++i) oc[nt][i][0] = oc[nt][i][1] = oc[nt][i][2] = oc[nt][i][3] = 0.f;
     }
-#pragma unroll
-    for (int y = 0; y < NG; ++y) unit[y] = pow2i(100);
   };
   if (n > 0) begin();
 
@@ -509,18 +517,11 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
     issue(i + C::STAGES - 1, out == ring ? ring + (C::STAGES - 1) * C::UNIT : out - C::UNIT);
     // ---- S^T = (c - 8) q^T of both tiles, scaled and shifted per group
     float x[2][NT][4];       // products: [tile][..][row g: heads 2t, 2t+1; row g + 8: ...]
-    uint32_t smax[NG];       // the largest of this lane's V scales, as bf16 bits in the low half
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const uint32_t base = out + tile * C::REC;
-      uint32_t kp[2 * NG], vp[2 * NG];  // parameters of this lane's tokens: [row g, g + 8][group]
+      uint32_t kp[2 * NG];  // parameters of this lane's tokens: [row g, g + 8][group]
       lds_params<NG>(base + 1024 * NG + g * 8 * NG, kp);
-      lds_params<NG>(base + 1088 * NG + g * 8 * NG, vp);
-#pragma unroll
-      for (int y = 0; y < NG; ++y) {
-        const uint32_t w = max_u16x2(vp[y], vp[NG + y]);
-        smax[y] = tile == 0 ? w : max_u16x2(smax[y], w);
-      }
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         const uint4 u = lds128(base + 512 * y + lane * 16);
@@ -569,18 +570,8 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
             for (int y = 0; y < NG; ++y) sts_word(out + tile * C::REC + 1088 * NG + ((2 * g + r) * NG + y) * 4, 0u);
           }
       __syncwarp();
-#pragma unroll
-      for (int y = 0; y < NG; ++y) smax[y] = 0u;  // without the masked slots: the result must not depend on them
-#pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
-        uint32_t vp[2 * NG];
-        lds_params<NG>(out + tile * C::REC + 1088 * NG + g * 8 * NG, vp);
-#pragma unroll
-        for (int y = 0; y < NG; ++y) smax[y] = max_u16x2(smax[y], max_u16x2(vp[y], vp[NG + y]));
-      }
     }
-    // ---- references: raised when a score passes m by 8, or a V scale 2^es by 2^6 (scales are not
-    // negative, so their bits order like the values)
+    // ---- references: raised when a score passes m by 8
     bool raise = false;
     float top[NT][2];
 #pragma unroll
@@ -590,44 +581,39 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
         top[nt][hh] = fmaxf(fmaxf(x[0][nt][hh], x[0][nt][2 + hh]), fmaxf(x[1][nt][hh], x[1][nt][2 + hh]));
         raise |= fmaf(top[nt][hh], fac[nt][hh], -m[nt][hh]) > 8.0f;
       }
-#pragma unroll
-    for (int y = 0; y < NG; ++y) raise |= fma_bf16(smax[y], __float_as_uint(unit[y]) >> 16, 0.f) > 64.0f;
     if (__any_sync(0xffffffffu, raise)) {
-      float down[NG];
 #pragma unroll
-      for (int y = 0; y < NG; ++y) {
-        float big = 0.f;
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          uint32_t vp[2 * NG];
-          lds_params<NG>(out + tile * C::REC + 1088 * NG + g * 8 * NG, vp);
-          big = fmaxf(big, fmaxf(bf16lo_to_f32(vp[y]), bf16lo_to_f32(vp[NG + y])));
-        }
-        const int es = 127 - (int)((__float_as_uint(unit[y]) >> 23) & 0xffu);
-        const int to = max(es, exponent_of(max_over_rows(big), 120));
-        down[y] = pow2i(max(es - to, -126));
-        unit[y] = pow2i(-to);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float al[2];
+        int less[2];  // 2^es falls with the weights seen so far, by whole powers of two
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const float to = fmaxf(m[nt][hh], max_over_rows(top[nt][hh]) * fac[nt][hh]);
-          const float al = to == -INFINITY ? 1.0f : ex2(m[nt][hh] - to);
+          al[hh] = to == -INFINITY ? 1.0f : ex2(m[nt][hh] - to);
+          less[hh] = to == -INFINITY ? 0 : (int)fminf(ceilf(to - m[nt][hh]), 240.0f);
           m[nt][hh] = to;
-          l[nt][hh] *= al;
+          l[nt][hh] *= al[hh];
+        }
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            zs[nt][y][hh] *= al;
+        for (int y = 0; y < NG; ++y) {
+          int es[2];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int was = unit_exponent(unit[nt][y], hh);
+            es[hh] = max(kDecKv4UnitMin, was - less[hh]);
+            const float down = al[hh] * pow2i(min(was - es[hh], 126));  // al is 0 where that is more than 126
+            zs[nt][y][hh] *= al[hh];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-              oc[nt][4 * y + mt][hh] *= al * down[y];
-              oc[nt][4 * y + mt][2 + hh] *= al * down[y];
+              oc[nt][4 * y + mt][hh] *= down;
+              oc[nt][4 * y + mt][2 + hh] *= down;
             }
           }
+          unit[nt][y] = unit_pair(es[0], es[1]);
         }
+      }
     }
-    // ---- P and the sums of its lane's tokens
+    // ---- P, the sums of its lane's tokens, and p s / 2^es in fp16
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -640,26 +626,86 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
         }
         l[nt][hh] += (x[0][nt][hh] + x[0][nt][2 + hh]) + (x[1][nt][hh] + x[1][nt][2 + hh]);
       }
+    uint32_t ps[2][NG][NT][2];  // [tile][group][..][row g, g + 8]: heads 2t, 2t + 1
+    uint32_t most = 0;
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      uint32_t vp[2 * NG];
+      lds_params<NG>(out + tile * C::REC + 1088 * NG + g * 8 * NG, vp);
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+        const uint32_t w0 = vp[y], w1 = vp[NG + y];
+        const float z0 = fma_bf16(w0, kBf16Eight, fma_bf16(w0 >> 16, kBf16One, 0.f));
+        const float z1 = fma_bf16(w1, kBf16Eight, fma_bf16(w1 >> 16, kBf16One, 0.f));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float* p = x[tile][nt];
+          const uint32_t u0 = unit[nt][y], u1 = u0 >> 16;
+          zs[nt][y][0] = fmaf(p[0], z0, fmaf(p[2], z1, zs[nt][y][0]));
+          zs[nt][y][1] = fmaf(p[1], z0, fmaf(p[3], z1, zs[nt][y][1]));
+          float s0 = fma_bf16(w0, u0, 0.f), s1 = fma_bf16(w0, u1, 0.f), s2 = fma_bf16(w1, u0, 0.f), s3 = fma_bf16(w1, u1, 0.f);
+          mul2(s0, s1, p[0], p[1]);
+          mul2(s2, s3, p[2], p[3]);
+          ps[tile][y][nt][0] = pack_f16x2(s0, s1);
+          ps[tile][y][nt][1] = pack_f16x2(s2, s3);
+          most = max_nan_f16x2(most, max_nan_f16x2(ps[tile][y][nt][0], ps[tile][y][nt][1]));
+        }
+      }
+    }
+    // A product of 2^15 or more (its half plus 0x0800 reaches the sign), or NaN, as 0 times an s / 2^es past fp32 is:
+    // 2^es becomes a power of two at most the largest product p s of the unit, which leaves 15 powers of
+    // two above it, and 14 below it before the fp16 steps grow.
+    if (__any_sync(0xffffffffu, ((most + 0x08000800u) & 0x80008000u) != 0)) {
+#pragma unroll
+      for (int y = 0; y < NG; ++y)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[2][2][2], big[2] = {0.f, 0.f};  // p s: [tile][row g, g + 8][head]
+#pragma unroll
+          for (int tile = 0; tile < 2; ++tile) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint32_t vp[1];
+              lds_words<1>(out + tile * C::REC + 1088 * NG + ((2 * g + r) * NG + y) * 4, vp);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                w[tile][r][hh] = x[tile][nt][2 * r + hh] * bf16lo_to_f32(vp[0]);
+                big[hh] = fmaxf(big[hh], w[tile][r][hh]);
+              }
+            }
+          }
+          int es[2];
+          float up[2];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int was = unit_exponent(unit[nt][y], hh);
+            es[hh] = max(was, exponent_of(max_over_rows(big[hh]), kDecKv4UnitMin, kDecKv4UnitMax));
+            up[hh] = pow2i(-es[hh]);
+            const float down = pow2i(max(was - es[hh], -126));
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              oc[nt][4 * y + mt][hh] *= down;
+              oc[nt][4 * y + mt][2 + hh] *= down;
+            }
+          }
+          unit[nt][y] = unit_pair(es[0], es[1]);
+#pragma unroll
+          for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) ps[tile][y][nt][r] = pack_f16x2(w[tile][r][0] * up[0], w[tile][r][1] * up[1]);
+        }
+    }
     // ---- O^T += (c - 8)^T (p s)^T
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const uint32_t base = out + tile * C::REC;
-      uint32_t vp[2 * NG];
-      lds_params<NG>(base + 1088 * NG + g * 8 * NG, vp);
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
-        const uint32_t w0 = vp[y], w1 = vp[NG + y], by = __float_as_uint(unit[y]) >> 16;
-        const float s0 = fma_bf16(w0, by, 0.f), s1 = fma_bf16(w1, by, 0.f);
-        const float z0 = fma_bf16(w0, kBf16Eight, fma_bf16(w0 >> 16, kBf16One, 0.f));
-        const float z1 = fma_bf16(w1, kBf16Eight, fma_bf16(w1 >> 16, kBf16One, 0.f));
         uint32_t b[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float* p = x[tile][nt];
-          b[nt][0] = movmatrix_trans(pack_f16x2(p[0] * s0, p[1] * s0));
-          b[nt][1] = movmatrix_trans(pack_f16x2(p[2] * s1, p[3] * s1));
-          zs[nt][y][0] = fmaf(p[0], z0, fmaf(p[2], z1, zs[nt][y][0]));
-          zs[nt][y][1] = fmaf(p[1], z0, fmaf(p[3], z1, zs[nt][y][1]));
+          b[nt][0] = movmatrix_trans(ps[tile][y][nt][0]);
+          b[nt][1] = movmatrix_trans(ps[tile][y][nt][1]);
         }
         const uint4 u = lds128(base + 512 * NG + 512 * y + 128 * t + 16 * (g ^ (2 * t)));
         uint32_t p01[4], p23[4];  // tokens b = 0, 1 and b = 2, 3: channels c of a half of the unit
@@ -701,7 +747,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
 #pragma unroll
           for (int y = 0; y < NG; ++y) {
             const float z = sum_over_rows(zs[nt][y][hh]);
-            const float up = 1.0f / unit[y];  // a power of two
+            const float up = pow2i(unit_exponent(unit[nt][y], hh));
             float v[8];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {

@@ -366,7 +366,9 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
 /*
  * attn_decode_paged_kv4 — attn_decode_paged over a 4-bit cache: o = softmax(scale q K^T) V with the
  * cached values x = s * c + m.  The codes enter the matrix products exactly; scores, running maxima
- * and sums are fp32, and the probabilities are rounded to 11 bits before P V.
+ * and sums are fp32.  Before P V the product of a probability and V's scale is rounded to fp16 (11 bits)
+ * relative to a power of two at most the largest such product so far of its query head and channel group:
+ * a product below 2^-14 of that power is off by at most 2^-25 of it instead.
  *
  *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned, not overlapping
  *   lse          device, fp32 [num_seqs, Hq] or NULL
