@@ -484,9 +484,11 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
         qf[nt][ks][0] = pack_f16x2(bf16lo_to_f32(raw[ks].x) * down, bf16hi_to_f32(raw[ks].x) * down);
         qf[nt][ks][1] = pack_f16x2(bf16lo_to_f32(raw[ks].y) * down, bf16hi_to_f32(raw[ks].y) * down);
       }
-      // this lane's e belongs to head g; the fragments of the products want heads 2t and 2t + 1
-      fac[nt][0] = a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t));
-      fac[nt][1] = a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t + 4));
+      // this lane's e belongs to head g; the fragments of the products want heads 2t and 2t + 1.  Kept above 0,
+      // where all scores are 0 to within 2^-21 anyway: -inf of a masked slot has to stay -inf.
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+        fac[nt][hh] = fmaxf(a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t + 4 * hh)), __int_as_float(1));
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         float s4[4];

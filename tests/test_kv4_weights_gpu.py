@@ -129,3 +129,20 @@ def test_scales_and_weights_that_run_against_one_another(Hq, Hkv, d, ps, wide, c
     o, lse, status = run_decode(q, pool, widen(table, ps) if wide else table, lens, ps, scale)
     assert status == 0
     check_weighted(o, lse, q, pool, table, lens, ps, scale)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,ps", FORMS)
+@pytest.mark.parametrize("scale", [1e-13, 1e-30, 1e-44])
+def test_zero_and_tiny_queries_at_a_tiny_scale(scale, Hq, Hkv, d, ps, wide, cuda_device):
+    # scores of 0: the mean of V, in rows that end inside a unit
+    rng = np.random.default_rng(d)
+    lens = [45, 700, 1]
+    table, num_pages = layout(rng, lens, ps)
+    pool = random_pool(rng, num_pages, Hkv, ps, d)
+    q = bf16(rng, (3, Hq, d))
+    q[:, 0] = 0
+    q[:, 1] *= 2.0 ** -110
+    o, lse, status = run_decode(q, pool, widen(table, ps) if wide else table, lens, ps, scale)
+    assert status == 0
+    check_weighted(o, lse, q, pool, table, lens, ps, scale)
