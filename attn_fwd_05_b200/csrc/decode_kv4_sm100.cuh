@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
   bool cut = f.z > 0;      // the segment began in an earlier warp's range
   uint32_t qf[NT][NG * 4][2];   // B fragments of q, scaled per head
   float qs[NT][NG][2];          // sum of the scaled q over a group, heads 2t and 2t + 1
-  float fac[NT][2];             // what turns the product with the scaled q into a log2 score
+  float fac[NT][2];             // what turns the product with the scaled q and K into a log2 score
+  uint32_t kmul;                // what K's parameters are multiplied by: bf16 2^-h, and 8 times that above
   float m[NT][2];               // reference of the exponentials (log2 score)
   float l[NT][2];               // sum of exponentials (this lane's tokens)
   float zs[NT][NG][2];          // sum of p (m + 8 s) (this lane's tokens)
@@ -460,6 +461,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
   auto rows_of = [&](int c) -> int { return min(C::ROWS, a.group - c % a.n_hg * C::ROWS); };
   auto begin = [&]() {
     const int nrows = rows_of(cc), hq0 = head_of(cc);
+    int e[NT], largest = -100;  // exponents of the largest elements
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint2 raw[NG * 4];
@@ -476,19 +478,15 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
       }
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // largest element to [2^13, 2^14): fp16 then holds every element down to 2^-31 of it exactly
-      const int e = exponent_of(__uint_as_float(big), -100, 127) - 13;
-      const float down = pow2i(-e);
+      // largest element to [2^13, 2^14): fp16 then holds every element down to 2^-30 of it exactly
+      e[nt] = exponent_of(__uint_as_float(big), -100, 127);
+      largest = max(largest, e[nt]);
+      const float down = pow2i(13 - e[nt]);
 #pragma unroll
       for (int ks = 0; ks < NG * 4; ++ks) {
         qf[nt][ks][0] = pack_f16x2(bf16lo_to_f32(raw[ks].x) * down, bf16hi_to_f32(raw[ks].x) * down);
         qf[nt][ks][1] = pack_f16x2(bf16lo_to_f32(raw[ks].y) * down, bf16hi_to_f32(raw[ks].y) * down);
       }
-      // this lane's e belongs to head g; the fragments of the products want heads 2t and 2t + 1.  Kept above 0,
-      // where all scores are 0 to within 2^-21 anyway: -inf of a masked slot has to stay -inf.
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-        fac[nt][hh] = fmaxf(a.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, 8 * t + 4 * hh)), __int_as_float(1));
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         float s4[4];
@@ -507,6 +505,20 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
 #pragma unroll
       for (int i = 0; i < NG * 4; ++i) oc[nt][i][0] = oc[nt][i][1] = oc[nt][i][2] = oc[nt][i][3] = 0.f;
     }
+    // K's parameters take the factor 2^-13 that q does not have, so that the products overflow only where q . K
+    // does; where scale times q is past fp32 (and K small, if the scores are finite), the factor stays in q
+    const bool far = __any_sync(0xffffffffu, exponent_of(a.scale_log2, -126, 127) + largest > 125);
+    const int h = far ? 0 : 13;
+    kmul = far ? kBf16One | kBf16Eight << 16 : (kBf16One | kBf16Eight << 16) - 0x06800680u;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        // this lane's e belongs to head g; the fragments of the products want heads 2t and 2t + 1.  Kept above 0,
+        // where all scores are 0 to within 2^-21 anyway: -inf of a masked slot has to stay -inf.
+        const int ex = __shfl_sync(0xffffffffu, e[nt], 8 * t + 4 * hh) - 13 + h;
+        fac[nt][hh] = fminf(fmaxf(a.scale_log2 * pow2i(ex), __int_as_float(1)), 3.4028234663852886e38f);
+      }
   };
   if (n > 0) begin();
 
@@ -532,9 +544,9 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, NT>::THREADS, DecKv4Cfg<D, NT>::C
         kv4_centred(u.y, lo[1]);
         kv4_centred(u.z, hi[0]);
         kv4_centred(u.w, hi[1]);
-        const float s0 = fma_bf16(kp[y], kBf16One, 0.f), s1 = fma_bf16(kp[NG + y], kBf16One, 0.f);
-        const float z0 = fma_bf16(kp[y], kBf16Eight, fma_bf16(kp[y] >> 16, kBf16One, 0.f));
-        const float z1 = fma_bf16(kp[NG + y], kBf16Eight, fma_bf16(kp[NG + y] >> 16, kBf16One, 0.f));
+        const float s0 = fma_bf16(kp[y], kmul, 0.f), s1 = fma_bf16(kp[NG + y], kmul, 0.f);
+        const float z0 = fma_bf16(kp[y], kmul >> 16, fma_bf16(kp[y] >> 16, kmul, 0.f));
+        const float z1 = fma_bf16(kp[NG + y], kmul >> 16, fma_bf16(kp[NG + y] >> 16, kmul, 0.f));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float c[4];

@@ -368,7 +368,8 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  * cached values x = s * c + m.  The codes enter the matrix products exactly; scores, running maxima
  * and sums are fp32.  Before P V the product of a probability and V's scale is rounded to fp16 (11 bits)
  * relative to a power of two at most the largest such product so far of its query head and channel group:
- * a product below 2^-14 of that power is off by at most 2^-25 of it instead.
+ * a product below 2^-14 of that power is off by at most 2^-25 of it instead.  q . K, scale * q . K, 2^-12 * scale * q
+ * and, over the tokens of a row, the sum of 256 |V| have to stay finite in fp32.
  *
  *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned, not overlapping
  *   lse          device, fp32 [num_seqs, Hq] or NULL

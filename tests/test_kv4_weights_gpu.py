@@ -1,5 +1,6 @@
-"""Decode over the 4-bit cache where tokens of very different V scales and weights meet.  The bounds follow
-the weights: a token that takes no part in a row's result must not cost the others their bits.
+"""Decode over the 4-bit cache where tokens of very different V scales and weights meet, and at the ends of
+the range of queries, keys and scales.  The bounds follow the weights: a token that takes no part in a
+row's result must not cost the others their bits.
 
 Per output element, from the roundings the kernel makes (w_j: the row's softmax weights, s_j: V's scale):
 * w_j s_j is rounded to fp16, 2^-11 of it, or 2^-25 of a power of two that is at most the largest such
@@ -20,7 +21,7 @@ import numpy as np
 import pytest
 
 from oracle import kv4
-from test_kv4_gpu import bf16, f64, layout, random_pool, run_decode, widen
+from test_kv4_gpu import BF, bf16, f64, layout, random_pool, run_decode, widen
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +147,41 @@ def test_zero_and_tiny_queries_at_a_tiny_scale(scale, Hq, Hkv, d, ps, wide, cuda
     o, lse, status = run_decode(q, pool, widen(table, ps) if wide else table, lens, ps, scale)
     assert status == 0
     check_weighted(o, lse, q, pool, table, lens, ps, scale)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,ps", FORMS)
+@pytest.mark.parametrize("q_exp,k_exp,scale_exp", [
+    (0, 112, -112),     # products of the unscaled query reach 2^124
+    (0, 112, -120), (-100, 112, -12), (100, 10, -110),
+    (120, -120, 0),
+    (125, -121, 5),     # the scale times the largest query is past fp32
+])
+def test_far_queries_keys_and_scales(q_exp, k_exp, scale_exp, Hq, Hkv, d, ps, wide, cuda_device):
+    rng = np.random.default_rng(abs(d + k_exp))
+    lens = [600, 33]
+    table, num_pages = layout(rng, lens, ps)
+    pool = random_pool(rng, num_pages, Hkv, ps, d)
+    for i, n in enumerate(lens):
+        set_params(pool, ps, d, False, table[i], range(n), factor=2.0 ** k_exp)
+    q = (bf16(rng, (2, Hq, d)).float() * 2.0 ** q_exp).to(BF)
+    scale = 2.0 ** scale_exp / math.sqrt(d)
+    o, lse, status = run_decode(q, pool, widen(table, ps) if wide else table, lens, ps, scale)
+    assert status == 0
+    check_weighted(o, lse, q, pool, table, lens, ps, scale)
+
+
+@pytest.mark.parametrize("exponent", [-100, 100])
+@pytest.mark.parametrize("wide", [False, True])
+def test_values_near_the_ends_of_the_range(wide, exponent, cuda_device):
+    # the sums of V stay finite in fp32; scales of 2^-104 are still normal numbers
+    rng = np.random.default_rng(5)
+    lens, d, ps = [300, 64], 128, 16
+    table, num_pages = layout(rng, lens, ps)
+    pool = random_pool(rng, num_pages, 2, ps, d)
+    for i, n in enumerate(lens):
+        set_params(pool, ps, d, True, table[i], range(n), factor=2.0 ** exponent)
+    q = bf16(rng, (2, 8, d))
+    o, lse, status = run_decode(q, pool, widen(table, ps) if wide else table, lens, ps, 0.09)
+    assert status == 0
+    check_weighted(o, lse, q, pool, table, lens, ps, 0.09)
