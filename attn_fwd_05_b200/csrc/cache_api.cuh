@@ -9,6 +9,37 @@
 
 namespace {
 
+// A buffer of a call: null or empty ones share no bytes with any other.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether a written buffer shares bytes with one that is read, or with another that is written: the
+// blocks of a call have no order in which the one would be done with before the other.
+template <size_t W, size_t R>
+bool any_overlap(const Span (&written)[W], const Span (&read)[R]) {
+  for (size_t i = 0; i < W; ++i) {
+    for (const Span& r : read)
+      if (overlap(written[i], r)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(written[i], written[j])) return true;
+  }
+  return false;
+}
+
+// n * each bytes, at most 2^62 (no address plus that wraps around).
+size_t span_bytes(long long n, size_t each) {
+  constexpr size_t kMost = size_t(1) << 62;
+  return n > 0 && each > kMost / (size_t)n ? kMost : (size_t)std::max(n, 0ll) * each;
+}
+
 bool kv4_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 bool cache_page_size(int p) { return p == 16 || p == 32 || p == 64; }
 
@@ -26,6 +57,10 @@ attn_status kv4_check(const void* pool, const int32_t* table, const int32_t* seq
   if ((long long)max_pages * page_size > kMaxTokens) return ATTN_ERR_INVALID_ARG;
   if (num_pages > 0x7fffffffLL / Hkv / (page_size / attn::kKv4Tok)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
+}
+
+Span kv4_pool_span(const void* pool, int page_size, int Hkv, int d, int num_pages) {
+  return {pool, span_bytes(num_pages, attn_kv4_page_bytes(Hkv, page_size, d))};
 }
 
 template <int NG>
@@ -164,6 +199,32 @@ attn_status pools_check(void* const* pools, int n_pools, size_t page_bytes, int 
   return ATTN_OK;
 }
 
+// Whether the workspace or a pool shares bytes with another buffer of a page operator.  Pools may be one and
+// the same (its pages are then moved twice, to the same places), not parts of one another.
+template <size_t W, size_t R>
+bool pools_overlap(const attn::PagePools& pp, int num_pages, const Span& workspace, const Span (&written)[W],
+                   const Span (&read)[R]) {
+  for (const Span& w : written)
+    if (overlap(workspace, w)) return true;
+  for (const Span& r : read)
+    if (overlap(workspace, r)) return true;
+  const uint8_t* sorted[attn::kMaxPools];
+  const size_t bytes = span_bytes(num_pages, (size_t)pp.page_bytes);
+  for (int i = 0; i < pp.n; ++i) {
+    const Span pool = {pp.base[i], bytes};
+    if (overlap(pool, workspace)) return true;
+    for (const Span& w : written)
+      if (overlap(pool, w)) return true;
+    for (const Span& r : read)
+      if (overlap(pool, r)) return true;
+    sorted[i] = pp.base[i];
+  }
+  std::sort(sorted, sorted + pp.n);
+  for (int i = 1; i < pp.n; ++i)
+    if (sorted[i] != sorted[i - 1] && overlap({sorted[i], bytes}, {sorted[i - 1], bytes})) return true;
+  return false;
+}
+
 // CTAs that share one page copy: one for every 16 KB, up to 32.
 int copy_parts(size_t page_bytes) {
   return (int)std::max<size_t>(1, std::min<size_t>(32, page_bytes / 16384));
@@ -181,11 +242,6 @@ bool small_table(int rows, int max_rows, int cols, int num_pages) {
 // pages of 16 KB that could move, 4 MB: 10.9 us against 12.3; of 32 KB: 16.2).
 int small_move(double copies, const attn::PagePools& pp, long long bytes) {
   return copies * pp.n * (double)pp.page_bytes <= (double)bytes;
-}
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
 }
 
 }  // namespace
@@ -212,11 +268,17 @@ attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int6
       (v_out && !aligned(v_out, 16)) || k_stride % 8 != 0 || v_stride % 8 != 0)
     return ATTN_ERR_ALIGNMENT;
   // written rows may be the rows read (each lane writes what it has read), not others of them
-  const size_t row = (size_t)Hkv * d * 2, in_k = (size_t)(num_new - 1) * k_stride * 2 + row,
-               in_v = (size_t)(num_new - 1) * v_stride * 2 + row, out = (size_t)num_new * row;
-  if ((k_out && (overlap(k_out, out, v, in_v) || (overlap(k_out, out, k, in_k) && (k_out != k || out != in_k)))) ||
-      (v_out && (overlap(v_out, out, k, in_k) || (overlap(v_out, out, v, in_v) && (v_out != v || out != in_v)))) ||
-      (k_out && v_out && overlap(k_out, out, v_out, out)))
+  const size_t row = (size_t)Hkv * d * 2, out = (size_t)num_new * row;
+  const Span in_k = {k, span_bytes(num_new - 1, (size_t)k_stride * 2) + row},
+             in_v = {v, span_bytes(num_new - 1, (size_t)v_stride * 2) + row};
+  const bool over_k = k_out == k && out == in_k.bytes, over_v = v_out == v && out == in_v.bytes;
+  const Span written[] = {{k_out, out}, {v_out, out}, kv4_pool_span(kv_pool, page_size, Hkv, d, num_pages)};
+  const Span read[] = {{block_table, span_bytes(num_seqs, (size_t)max_pages_per_seq * 4)},
+                       {seq_lens, (size_t)num_seqs * 4},
+                       {cu_new, ((size_t)num_seqs + 1) * 4}};
+  if (any_overlap(written, read) || overlap(written[2], in_k) || overlap(written[2], in_v) ||
+      (!over_k && overlap(written[0], in_k)) || overlap(written[0], in_v) || (!over_v && overlap(written[1], in_v)) ||
+      overlap(written[1], in_k))
     return ATTN_ERR_INVALID_ARG;
   attn::Kv4AppendArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -260,6 +322,13 @@ attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, con
   if (num_seqs == 0 || N == 0) return ATTN_OK;
   if (k == nullptr || v == nullptr) return ATTN_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_ALIGNMENT;
+  // k may be v: a lane writes V's values after K's
+  const size_t out = span_bytes((long long)num_seqs * Hkv, (size_t)N * d * 2);
+  const Span written[] = {{k, out}, {k == v ? nullptr : v, out}};
+  const Span read[] = {kv4_pool_span(kv_pool, page_size, Hkv, d, num_pages),
+                       {block_table, span_bytes(num_seqs, (size_t)max_pages_per_seq * 4)},
+                       {seq_lens, (size_t)num_seqs * 4}};
+  if (any_overlap(written, read)) return ATTN_ERR_INVALID_ARG;
   attn::Kv4GatherArgs a;
   std::memset(&a, 0, sizeof(a));
   a.pool = static_cast<const uint8_t*>(kv_pool);
@@ -273,7 +342,7 @@ attn_status attn_kv4_gather(const void* kv_pool, const int32_t* block_table, con
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.max_pages = max_pages_per_seq;
-  // N may be larger than any row: records past a row's capacity have no work
+  // N may be larger than any row: the warps of records past a row's end return
   const long long nrec = ((long long)N + 15) / 16;
   const long long units = nrec * num_seqs;
   if (units > 0x7fffffffLL * attn::kKv4GatherWarps / Hkv) return ATTN_ERR_INVALID_ARG;
@@ -311,6 +380,13 @@ attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int3
   const DecKv4Layout L = kv4_layout(num_seqs, group, d);
   if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  const size_t rows = (size_t)num_seqs * Hq;
+  const Span written[] = {{o, rows * d * 2}, {lse, rows * 4}, {workspace, L.total}};
+  const Span read[] = {{q, rows * d * 2},
+                       kv4_pool_span(kv_pool, page_size, Hkv, d, num_pages),
+                       {block_table, span_bytes(num_seqs, (size_t)max_pages_per_seq * 4)},
+                       {seq_lens, (size_t)num_seqs * 4}};
+  if (any_overlap(written, read)) return ATTN_ERR_INVALID_ARG;
   attn::DecKv4Args a;
   std::memset(&a, 0, sizeof(a));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -360,22 +436,23 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
   attn::PagePools pp;
   const attn_status chk = pools_check(pools, n_pools, page_bytes, num_pages, &pp);
   if (chk != ATTN_OK) return chk;
-  const size_t in_bytes = (size_t)num_seqs * max_pages_per_seq * 4, out_bytes = (size_t)new_rows * new_max_pages * 4;
   if ((num_seqs > 0 && (block_table == nullptr || seq_lens == nullptr)) ||
       (new_rows > 0 && (parents == nullptr || new_table == nullptr || new_lens == nullptr)))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(add_tokens, 4) ||
       !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(n_free, 4))
     return ATTN_ERR_ALIGNMENT;
-  // rows are read while others are written
-  if (overlap(block_table, in_bytes, new_table, out_bytes) ||
-      overlap(seq_lens, (size_t)num_seqs * 4, new_lens, (size_t)new_rows * 4) ||
-      overlap(parents, (size_t)new_rows * 4, new_lens, (size_t)new_rows * 4) ||
-      overlap(add_tokens, (size_t)new_rows * 4, new_lens, (size_t)new_rows * 4))
-    return ATTN_ERR_INVALID_ARG;
   const PagesLayout L = pages_layout(num_pages, new_rows);
+  const size_t per_row = (size_t)new_rows * 4;
+  const Span written[] = {{new_table, span_bytes(new_rows, (size_t)new_max_pages * 4)}, {new_lens, per_row}, {n_free, 4}};
+  const Span read[] = {{block_table, span_bytes(num_seqs, (size_t)max_pages_per_seq * 4)},
+                       {seq_lens, (size_t)num_seqs * 4},
+                       {parents, per_row},
+                       {add_tokens, per_row}};
+  if (any_overlap(written, read)) return ATTN_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  if (pools_overlap(pp, num_pages, {workspace, L.total}, written, read)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   attn::ForkArgs a;
@@ -434,11 +511,14 @@ attn_status attn_pages_compact(const int32_t* block_table, const int32_t* seq_le
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(new_table, 4) || !aligned(page_map, 4) ||
       !aligned(n_live, 4))
     return ATTN_ERR_ALIGNMENT;
-  const size_t bytes = (size_t)num_seqs * max_pages_per_seq * 4;
-  if (block_table != new_table && overlap(block_table, bytes, new_table, bytes)) return ATTN_ERR_INVALID_ARG;
   const PagesLayout L = pages_layout(num_pages, num_seqs);
+  const size_t bytes = span_bytes(num_seqs, (size_t)max_pages_per_seq * 4);
+  const Span written[] = {{new_table, bytes}, {page_map, (size_t)num_pages * 4}, {n_live, 4}};
+  const Span read[] = {{block_table == new_table ? nullptr : block_table, bytes}, {seq_lens, (size_t)num_seqs * 4}};
+  if (any_overlap(written, read)) return ATTN_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < L.total) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  if (pools_overlap(pp, num_pages, {workspace, L.total}, written, read)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   attn::CompactArgs a;

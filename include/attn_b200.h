@@ -310,6 +310,9 @@ size_t attn_decode_paged_noalloc_max_scratch(void);
  *                  half of the word, m in the high half
  * page_size is 16, 32 or 64 and d is 64, 128 or 256; num_pages * Hkv * page_size / 16 < 2^31,
  * and max_pages_per_seq * page_size (like attn_kv4_gather's N) is at most 2^30.
+ *
+ * The entry points below refuse (ATTN_ERR_INVALID_ARG) a buffer that is written and shares bytes with another
+ * buffer of the call, but for what is said at the argument.
  */
 
 /* Bytes of one page of a 4-bit pool: Hkv * page_size * d * 9 / 8, or 0 for unsupported sizes. */
@@ -330,7 +333,7 @@ size_t attn_kv4_page_bytes(int Hkv, int page_size, int d);
  *   k_out, v_out device, bf16 [num_new, Hkv, d] (dense, 16-byte aligned) or NULL: written with the
  *                values the cache now stands for, rounded to bf16, so that a prompt's own attention can
  *                see exactly what later decode steps will see.  k_out may be a dense k itself and v_out a
- *                dense v; any other overlap of an output with k, v or the other output is refused
+ *                dense v
  * A slot must not be written by two tokens of one call (pages shared between rows are for reading:
  * see attn_pages_fork).  A table entry in use outside [0, num_pages) is skipped and latches
  * ATTN_ERR_BAD_PAGE; a sequence whose seq_lens or cu_new entries are out of range is skipped and
@@ -347,7 +350,7 @@ attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int6
  *
  *   k, v         device, bf16 [num_seqs, Hkv, N, d], 16-byte aligned: tokens 0 .. min(seq_lens[s], N) - 1
  *                of every sequence are written with the cached values rounded to bf16; rows past a
- *                sequence's end are left as they were
+ *                sequence's end are left as they were.  k may be v, which then holds the values of V
  * Other arguments as in attn_kv4_append.  Tokens of a table entry outside [0, num_pages) are skipped
  * (ATTN_ERR_BAD_PAGE is latched), as is a sequence with a length outside
  * [0, max_pages_per_seq * page_size] (ATTN_ERR_INVALID_ARG).
@@ -371,7 +374,7 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  * a product below 2^-14 of that power is off by at most 2^-25 of it instead.  q . K, scale * q . K, 2^-12 * scale * q
  * and, over the tokens of a row, the sum of 256 |V| have to stay finite in fp32.
  *
- *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned, not overlapping
+ *   q, o         device, bf16 [num_seqs, Hq, d], 16-byte aligned
  *   lse          device, fp32 [num_seqs, Hq] or NULL
  *   workspace    device scratch of at least attn_decode_paged_kv4_workspace_size(...) bytes, 256-byte
  *                aligned, overwritten; two calls in flight at once need two workspaces
@@ -393,7 +396,8 @@ attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int3
  * entries, and free otherwise.  Several pools (K and V, every layer) can share one table:
  *
  *   pools       HOST array of n_pools (0 .. 128) device pointers, 16-byte aligned, each to num_pages pages
- *               of page_bytes bytes (a multiple of 16); copied during the call
+ *               of page_bytes bytes (a multiple of 16); the array is copied during the call.  A pool may be
+ *               listed twice, but not overlap another in part
  *   page_size   tokens per page (any positive number; a row's pages hold at most 2^30 tokens)
  *
  * attn_pages_workspace_size — scratch of attn_pages_fork (rows = new_rows) and attn_pages_compact
@@ -410,8 +414,8 @@ size_t attn_pages_workspace_size(int num_pages, int rows);
  *   add_tokens  device, int32 [new_rows] or NULL (zeros): new_lens[i] = seq_lens[parents[i]] + add_tokens[i];
  *               a negative number drops the last tokens
  *   new_table   device, int32 [new_rows, new_max_pages], new_max_pages >= max_pages_per_seq (written; -1 past
- *               each row's pages); must not overlap block_table
- *   new_lens    device, int32 [new_rows] (written); must not overlap the inputs
+ *               each row's pages)
+ *   new_lens    device, int32 [new_rows] (written)
  *   n_free      device, int32 [1] or NULL: pages left free
  *
  * Full pages are shared by the rows that continue them.  The part-filled page after a row's kept
@@ -436,7 +440,7 @@ attn_status attn_pages_fork(const int32_t* block_table, const int32_t* seq_lens,
  * n, in ascending order.
  *
  *   new_table  device, int32 [num_seqs, max_pages_per_seq] (written; -1 past each row's pages); may be
- *              block_table itself, must not overlap it otherwise
+ *              block_table itself
  *   page_map   device, int32 [num_pages] (written): new number of each page, -1 where it was free
  *   n_live     device, int32 [1] or NULL: n
  * A length out of range counts as 0 and a table entry in use outside [0, num_pages) becomes -1; these
