@@ -397,7 +397,9 @@ attn_status attn_decode_paged_kv4(const void* q, const void* kv_pool, const int3
  *
  *   pools       HOST array of n_pools (0 .. 128) device pointers, 16-byte aligned, each to num_pages pages
  *               of page_bytes bytes (a multiple of 16); the array is copied during the call.  A pool may be
- *               listed twice, but not overlap another in part
+ *               listed twice, but not overlap another in part.  More pools than 128 take several calls with the
+ *               same old table, lengths and parents: the new table comes out the same each time (so not in
+ *               place: the old table has to last until the last of them)
  *   page_size   tokens per page (any positive number; a row's pages hold at most 2^30 tokens)
  *
  * attn_pages_workspace_size — scratch of attn_pages_fork (rows = new_rows) and attn_pages_compact

@@ -43,3 +43,36 @@ def test_a_pool_listed_twice_is_moved_once(shapes, cuda_device):
     assert not np.array_equal(got[0][0], got[0][1])
     for a, b in zip(*got):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("more", [0, 2100])
+def test_many_pools_in_several_calls(more, cuda_device):
+    # 160 pools that share a table, 128 and 32 a call, against all of them moved in calls of one
+    rng = np.random.default_rng(53)
+    table, lens, num_pages = random_rows(rng, 5, 16, 6, 40, lo=1)
+    table = np.concatenate([table, np.full((5, more), -1, dtype=np.int32)], axis=1)
+    fill = torch.from_numpy(rng.integers(0, 256, (160, num_pages, 48), dtype=np.uint8)).to(dev())
+    parents = ints([4, 4, 0, 2, 2, 1])
+
+    def step(pools, sizes):
+        tables, at = [], 0
+        ws = torch.empty(ab.attn_pages_workspace_size(num_pages, 6), dtype=torch.uint8, device=dev())
+        nt, nl = torch.empty((6, 6 + more), dtype=torch.int32, device=dev()), ints(np.zeros(6))
+        for n in sizes:
+            ab.attn_pages_fork(ints(table), ints(lens), parents, None, nt, nl, 16, pools[at:at + n], ws)
+            tables.append(nt.clone())
+            at += n
+        at = 0
+        ct, pm = torch.empty_like(nt), ints(np.zeros(num_pages))
+        for n in sizes:
+            ab.attn_pages_compact(nt, nl, ct, pm, 16, pools[at:at + n], ws)
+            tables.append(ct.clone())
+            at += n
+        assert ab.attn_get_device_status() == 0
+        assert all(torch.equal(t, tables[0]) for t in tables[:len(sizes)])
+        assert all(torch.equal(t, tables[-1]) for t in tables[len(sizes):])
+        return tables[0], tables[-1], torch.stack(pools)
+
+    a, b = fill.clone(), fill.clone()
+    for x, y in zip(step(list(a), [128, 32]), step(list(b), [1] * 160)):
+        assert torch.equal(x, y)
