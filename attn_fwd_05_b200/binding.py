@@ -96,8 +96,10 @@ def load_library() -> ctypes.CDLL:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:  # the handle alone: building a torch.cuda.Stream costs 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        # the handle alone where this PyTorch gives it: building a torch.cuda.Stream costs 3 us a call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
