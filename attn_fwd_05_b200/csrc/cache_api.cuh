@@ -119,7 +119,8 @@ struct DecKv4Layout {
 };
 
 // Query heads of a segment: 8 columns of an MMA, or 16 where a group has more than 8 heads and
-// the accumulators leave room (16 rows of up to 8192 tokens, 8 groups of 16: 38.4 us instead of 43.1).
+// the accumulators leave room (16 rows of up to 8192 tokens, 8 groups of 16: 38.7 us instead of 42.2; 32 rows at
+// d = 64: 46.2 instead of 56.3).
 int kv4_head_tiles(int group, int d) { return group > 8 && d <= 128 ? 2 : 1; }
 
 DecKv4Layout kv4_layout(int S, int group, int d) {
@@ -135,10 +136,10 @@ DecKv4Layout kv4_layout(int S, int group, int d) {
 template <int D, int NT>
 attn_status launch_decode_kv4(const attn::DecKv4Args& a, cudaStream_t st, int slot) {
   using C = attn::DecKv4Cfg<D, NT>;
-  // Few short rows go out in one launch, a cluster a segment: 8.3 us instead of 12.3 for one row of 512
-  // tokens with 8 KV heads, 14.4 instead of 20.6 for 8 rows of 2048.  Not with fewer than 4 CTAs a
-  // segment (16 rows of 512: 14.5 against 14.4, with d = 256 20.5 against 20.5), and not for rows that
-  // could be longer than 1024 tokens a CTA (one row of 16384: 21.7 against 18.5), where the even cut over
+  // Few short rows go out in one launch, a cluster a segment: 7.4 us instead of 10.6 for one row of 512
+  // tokens with 8 KV heads, 13.4 instead of 16.9 for 8 rows of 2048.  Not with fewer than 4 CTAs a
+  // segment (16 rows of 512: 14.6 against 13.5, with d = 256 19.3 against 19.4), and not for rows that
+  // could be longer than 1024 tokens a CTA (one row of 16384: 20.8 against 19.5), where the even cut over
   // all SMs gains more than the launch.  The table's width bounds the lengths, which are on the device.
   const long long segments = (long long)a.S * a.Hkv * a.n_hg, resident = (long long)sm_count() * C::CTAS_PER_SM;
   int cluster = attn::kDecKv4MaxCluster;

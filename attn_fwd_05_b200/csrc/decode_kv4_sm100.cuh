@@ -30,12 +30,14 @@
 // others leave partials (at most two per warp) that the merge kernel joins by log-sum-exp.  Few short
 // rows take one launch in place of two: a cluster of CTAs per segment, which joins them itself.
 //
-// What bounds it: issue slots.  A 16-token tile of 128 channels costs a warp 355 instructions (216 with
-// 64 channels), 16 of them MMAs, each of which holds its scheduler's issue port for about 8 cycles, while
-// HBM delivers a tile per scheduler every 400 cycles.  64 sequences of 512 to 32768 tokens, 64
-// query heads on 8, d = 128: 273 us, 4.9 TB/s of cache; the loads alone (no arithmetic) take 213 us,
-// without the conversion of codes 243 us.  Two rows of 131071 tokens: 76 us; 96 rows of up to 2048
-// tokens, 16 heads, d = 64: 41 us.  Tried and slower: the conversion into 8-bit operands for e4m3 MMAs
+// What bounds it: mostly issue slots.  A 16-token tile of 128 (64) channels costs a warp 336 (233) instructions, its
+// share of a segment's start and end included, 16 (8) of them MMAs, each of which holds its scheduler's
+// issue port for about 8 cycles, while HBM delivers a tile per scheduler every 400 cycles.  The counters
+// show 61 % of the slots taken and the MMAs' hold is another 21 %; with 64 channels it is 60 % and 15 %, and the
+// rest are the waits of short segments.  64 sequences of 512 to 32768 tokens, 64 query heads on 8, d = 128: 287
+// to 299 us replayed (the GPU at its power limit), 317 us called, 4.2 TB/s of cache; the loads alone (no
+// arithmetic) take 213 us.  Two rows of 131071 tokens: 79 us; 96 rows of up to 2048 tokens, 16 heads, d = 64:
+// 43 us.  Tried and slower, when the first batch took 273 us: the conversion into 8-bit operands for e4m3 MMAs
 // (this MMA becomes conversions and f16 MMAs on this GPU: 450 us), one CTA of 16 warps (no gain), and
 // tcgen05 with the codes expanded into shared memory (709 us: write, expansion and the operand's read
 // take 912 cycles of shared memory per 128 tokens, of which HBM delivers as many in 794).
@@ -68,11 +70,12 @@ struct DecKv4Cfg {
   static constexpr int REC = kv4_record_bytes(D);
   static constexpr int UNIT = 2 * REC;  // a unit of work: 32 tokens, two records
   static constexpr int WARPS = 4;
-  // resident CTAs (one fewer: 301 us instead of 273 for the batch above, 43 instead of 41 at d = 64; one
-  // more, squeezed into 128 and 96 registers: 282 against 281, two long rows 80 against 76, 43 against 41)
+  // resident CTAs (one fewer: 337 us instead of 301 for the batch above, 43 instead of 40.6 at d = 64, 52 instead of
+  // 44 at d = 256; one more, squeezed into 128 and 96 registers, gained nothing: 282 against 281, 43 against 41
+  // before p s had a scale of its own per head)
   static constexpr int CTAS_PER_SM = D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : 2);
   // units in flight a warp, the one at work included: 18 KB and less (d = 256, 16 rows of up to 8192
-  // tokens: 46 us with 3 and 44 with 2; d = 128: 273 with 3, 275 with 4)
+  // tokens: 46 us with 3 and 44 with 2; d = 128: 301 with 3, 302 with 4)
   static constexpr int STAGES = D == 64 ? 4 : (D == 128 ? 3 : 2);
   static constexpr int SMEM = WARPS * STAGES * UNIT;
   static constexpr int THREADS = WARPS * 32;
@@ -169,7 +172,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // The pairs (nibble i of the low half, nibble i of the high half) of a word as fp16 c - 8,
-// i = 0..3.  1024 + c - 1032 and (1024 + 16 c) / 16 - 72 are exact.
+// i = 0..3.  1024 + c - 1032 and (1024 + 16 c) / 16 - 72 are exact.  (Integers as the mantissa bits of 1024, for
+// 4-bit weights: Kim et al. 2022, "Who Says Elephants Can't Run".)
 __device__ __forceinline__ void kv4_centred(uint32_t w, uint32_t (&p)[4]) {
   const uint32_t w8 = w >> 8;
   uint32_t x0, x1, x2, x3;
@@ -236,7 +240,7 @@ struct Kv4Cursor {
 
 // The ranges are cut by cost: a segment of nt units counts nt + kDecKv4SegCost, the surplus in front
 // of its first unit (many short rows would otherwise make their warps the last to finish: 96 rows of
-// up to 2048 tokens with 16 heads took 59 us without it and 41 with it).
+// up to 2048 tokens with 16 heads take 58 us without it and 40.6 with it).
 //
 // Finds the first units of this CTA's warps: first[w] = {s, c, t, units of the range} (0 units: no
 // work).  Every thread of the block calls it.  CTA 0 also leaves the prefix of costs for the merge.

@@ -245,7 +245,8 @@ __device__ __forceinline__ int kv4_find_seq(const int32_t* cu, int S, long long 
 // heads, d = 128: 359 us with one head a warp, 272 with 2, 229 with 4, 216 with 8; a decode step of 64
 // tokens 6.2 us with one and 14.4 with 8), and fetches the next head's rows while it works on one
 // (without: 254).  Small blocks and a few spilled words leave room for 20 warps an SM instead of
-// 16: 199 us, 5.6 TB/s (24 warps with 108 bytes spilled: 245); d = 256: 413 us instead of 505.
+// 16: 199 us, 5.6 TB/s (24 warps with 108 bytes spilled: 245); d = 256: 413 us instead of 505.  (Replayed
+// graphs; called one after another the prompts take 212 us, the step 11.)
 template <int NG>
 __global__ void __launch_bounds__(kKv4AppendThreads, NG == 1 ? 6 : (NG == 2 ? 5 : 3))
     attn_kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {

@@ -332,8 +332,9 @@ size_t attn_kv4_page_bytes(int Hkv, int page_size, int d);
  *                cu_new[num_seqs] on are padding, and their k_out and v_out rows are left as they were
  *   k_out, v_out device, bf16 [num_new, Hkv, d] (dense, 16-byte aligned) or NULL: written with the
  *                values the cache now stands for, rounded to bf16, so that a prompt's own attention can
- *                see exactly what later decode steps will see.  k_out may be a dense k itself and v_out a
- *                dense v
+ *                see exactly what later decode steps will see.  They are token by token like k and v; for
+ *                attn_fwd, which takes [B, Hkv, Nk, d], more than one KV head has to be transposed.  k_out
+ *                may be a dense k itself and v_out a dense v
  * A slot must not be written by two tokens of one call (pages shared between rows are for reading:
  * see attn_pages_fork).  A table entry in use outside [0, num_pages) is skipped and latches
  * ATTN_ERR_BAD_PAGE; a sequence whose seq_lens or cu_new entries are out of range is skipped and
@@ -350,7 +351,8 @@ attn_status attn_kv4_append(const void* k, const void* v, int64_t k_stride, int6
  *
  *   k, v         device, bf16 [num_seqs, Hkv, N, d], 16-byte aligned: tokens 0 .. min(seq_lens[s], N) - 1
  *                of every sequence are written with the cached values rounded to bf16; rows past a
- *                sequence's end are left as they were.  k may be v, which then holds the values of V
+ *                sequence's end are left as they were (attn_fwd, which has no lengths, takes a sequence
+ *                of its own call, N its length).  k may be v, which then holds the values of V
  * Other arguments as in attn_kv4_append.  Tokens of a table entry outside [0, num_pages) are skipped
  * (ATTN_ERR_BAD_PAGE is latched), as is a sequence with a length outside
  * [0, max_pages_per_seq * page_size] (ATTN_ERR_INVALID_ARG).
